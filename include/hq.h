@@ -361,9 +361,157 @@ hq_status_t hq_step_search(const void* x, hq_dtype_t dtype, int64_t rows, int64_
                            int32_t kv, int64_t kv_S, int32_t max_probes, float tol_bps, hq_rate_result_t* result,
                            void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Operators on 8-bit floating-point blocks.  Codes are e4m3 (4 exponent bits, 3 fraction bits, largest
+ * value 448, no infinities); a block of values shares one binary32 scale and a value is its code
+ * times the scale.  The quantizers here write power-of-two scales: the smallest 2^e, e in [-40, 40],
+ * with max |x| <= 448 * 2^e (2^-40 for a block of zeros), and the code nearest to x / 2^e, ties to
+ * the even code.  Larger values saturate at 448 * 2^40 and report HQ_ERR_RANGE.
+ *   - ws may be NULL where an entry point says so; device errors are not recorded then.  With ws, the
+ *     status is written by the call's own kernels (no clearing launch) and read with hq_status_read.
+ *   - The current device of the calling thread is put back before these entry points return.
+ * ------------------------------------------------------------------------------------------------ */
+
+/* Workspace bytes of hq_fp8_quantize, hq_gemm_fp8 and hq_kv8_append when they are given one. */
+size_t hq_fp8_workspace_bytes(void);
+
+/*
+ * Quantize x[rows, cols] (device, row pitch ldx elements, bf16 or fp32) to e4m3.
+ *   block  1: one scale for each row and 128 columns (activations); 128: one for each 128 x 128 block
+ *          (weights); the last blocks may be partial
+ *   q      [rows, ldq] codes, ldq = cols rounded up to a multiple of 16, 16-byte aligned; the columns
+ *          past cols are zeros
+ *   scale  [ceil(cols / 128), ceil(rows / block)] fp32
+ * A block with NaN or infinity is coded as zeros (HQ_ERR_NONFINITE, detail = blocks).  ws may be NULL.
+ */
+hq_status_t hq_fp8_quantize(const void* x, hq_dtype_t dtype, int64_t rows, int64_t cols, int64_t ldx, int32_t block,
+                            uint8_t* q, int64_t ldq, float* scale, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Block-scaled e4m3 GEMM on the tensor cores:
+ *   Y[m, n] = sum_t sa[t, m] sw[t, n / 128] sum_{k = 128 t}^{min(128 t + 127, K - 1)} A[m, k] W[n, k]
+ * A [M, K] and W [N, K] codes with row pitches lda and ldw (multiples of 16, 16-byte aligned; bytes
+ * between K and the pitch are not read), sa [ceil(K / 128), M], sw [ceil(K / 128), ceil(N / 128)] as
+ * written by hq_fp8_quantize with block 1 and 128 (any finite scales are accepted), Y [M, N] bf16 or
+ * fp32.  Every size from 1 up (K <= 2^20).  Block sums and the sum over blocks are binary32, in the
+ * order of t.  ws may be NULL; a bounded wait that ran out reports HQ_ERR_TIMEOUT there.
+ */
+hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W, int64_t ldw,
+                        const float* sw, int64_t N, int64_t K, void* Y, hq_dtype_t ydtype, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/*
+ * An e4m3 KV cache in pages: k and v are [pages][heads][page][dim] codes (16-byte aligned), k_scale
+ * and v_scale [pages][heads] one fp32 scale for each page and head (positive, in [2^-40, 2^40]).
+ * dim 64 or 128, page 16, 32, 64 or 128 tokens (HQ_ERR_UNSUPPORTED otherwise).  A sequence is a row
+ * of a page table (int32 page numbers) and a length (int32, device): slot j lies in page table[j / page]
+ * at row j % page.  Page numbers outside the pool and lengths outside the table report HQ_ERR_RANGE;
+ * slots of such pages are not read or written (attention treats them as unseen) and lengths are
+ * clamped.  Bytes behind a sequence's length are never used: they may hold anything.
+ */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t pages;
+    int32_t heads, page, dim;
+} hq_kv8_t;
+
+/*
+ * Append: tokens 0 .. n_new[b] - 1 of k, v [B, heads, S, dim] (element strides of b, head, token; dim
+ * contiguous; base and strides multiples of 16 bytes) become slots lens[b] .. of sequence b.  A page's
+ * scale becomes the larger of what its earlier tokens had and what the new ones need; where it grows,
+ * the earlier codes q follow as the code nearest to q s_old / s_new.  A token's vector with NaN or
+ * infinity is kept as zeros (HQ_ERR_NONFINITE, detail = vectors).  n_new NULL: S for every sequence.
+ * Tokens past the table are dropped (HQ_ERR_RANGE).  lens is not changed.  A page that is appended to
+ * belongs to one sequence only.  ws may be NULL (else hq_fp8_workspace_bytes()).
+ */
+typedef struct {
+    hq_kv8_t cache;
+    const void* k;
+    const void* v;
+    hq_dtype_t dtype;
+    int64_t B, S;
+    int64_t k_stride[3], v_stride[3];
+    const int32_t* table;
+    int64_t table_stride, max_pages;
+    const int32_t* lens;
+    const int32_t* n_new;
+} hq_kv8_append_t;
+hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention over the cache: q, out [B, Hq, Sq, dim] bf16 (element strides of b, head, token; multiples
+ * of 8, 16-byte aligned bases), query head i reads key head i / (Hq / heads).
+ *   lens      [B] slots of each sequence (the queries' own tokens among them)
+ *   q_lens    [B] queries of each sequence, NULL: Sq; rows behind them are left as they were
+ *   causal    0: a query sees all lens[b] slots; 1: query i of m sees slots 0 .. lens[b] - m + i
+ *   lse       [B, Hq, Sq] fp32 (strides of b and head) natural logarithm of the sum of exp(scale q.k),
+ *             or NULL.  A row that sees nothing gives zeros and -infinity.
+ *   weights   [B, heads, L] fp32 (strides of b and head), or NULL: for every slot j < lens[b] the sum
+ *             of the probabilities it received from its head's rows, added to weights_in (same shape;
+ *             NULL: 0; may be weights itself).  Slots behind are left as they were; slots j >= L are
+ *             dropped (HQ_ERR_RANGE).
+ *   ws        hq_kv8_attend_workspace_bytes(B, Hq, Sq, dim, weights != NULL) bytes, 256-byte aligned
+ * Products take bf16 queries and codes exactly and accumulate in binary32; probabilities enter the
+ * second product as binary16.  B <= 4096.  The result does not depend on the other sequences' content.
+ */
+typedef struct {
+    hq_kv8_t cache;
+    const void* q;
+    void* out;
+    int64_t B, Hq, Sq;
+    int64_t q_stride[3], out_stride[3];
+    const int32_t* table;
+    int64_t table_stride, max_pages;
+    const int32_t* lens;
+    const int32_t* q_lens;
+    float scale;
+    int32_t causal;
+    float* lse;
+    int64_t lse_stride[2];
+    const float* weights_in;
+    float* weights;
+    int64_t win_stride[2], w_stride[2];
+    int64_t L;
+} hq_kv8_attend_t;
+size_t hq_kv8_attend_workspace_bytes(int64_t B, int64_t Hq, int64_t Sq, int32_t dim, int32_t weights);
+hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction by accumulated attention weight.  Of each sequence and head, the last min(recent, budget)
+ * slots stay, and of the others those with the largest weights (the lower slot among equals, NaN below
+ * everything) until budget slots are kept; sequences of budget slots or fewer keep all.  Each head
+ * keeps its own slots.  They are moved, in order, to slots 0 .. of the pages to_table[b] (which no
+ * sequence of the call reads), a new page's scale being the largest of its tokens' old ones and
+ * codes following as in hq_kv8_append; out_lens[b] = min(lens[b], budget) (may be lens itself).
+ * weights [B, heads, L] and out_weights [B, heads, >= budget] (strides of b and head; NULL: not
+ * wanted; another buffer than weights) hold the slots' weights before and after.
+ * ws: hq_kv8_evict_workspace_bytes(B, heads, budget) bytes.
+ */
+typedef struct {
+    hq_kv8_t cache;
+    int64_t B;
+    const int32_t* table;
+    int64_t table_stride, max_pages;
+    const int32_t* lens;
+    const float* weights;
+    int64_t w_stride[2];
+    int64_t L;
+    int64_t budget, recent;
+    const int32_t* to_table;
+    int64_t to_stride, to_pages;
+    int32_t* out_lens;
+    float* out_weights;
+    int64_t ow_stride[2];
+} hq_kv8_evict_t;
+size_t hq_kv8_evict_workspace_bytes(int64_t B, int32_t heads, int64_t budget);
+hq_status_t hq_kv8_evict(const hq_kv8_evict_t* p, void* ws, size_t ws_bytes, void* stream);
+
 /*
  * Synchronise `stream`, then read the status word of `ws`: returns HQ_OK or the most severe
- * device error (TIMEOUT, CORRUPT, CAPACITY, NONFINITE in that order) and, if detail is not NULL,
+ * device error (TIMEOUT, CORRUPT, CAPACITY, RANGE, NONFINITE in that order) and, if detail is not NULL,
  * its detail value (capacity: words needed; non-finite: tiles affected).
  */
 hq_status_t hq_status_read(const void* ws, void* stream, int64_t* detail);

@@ -13,6 +13,7 @@
 #include "hq_common.cuh"
 #include "hq_decode.cuh"
 #include "hq_encode.cuh"
+#include "hq_fp8.cuh"
 #include "hq_launch.h"
 
 namespace hq {
@@ -47,14 +48,15 @@ EncodeTiledFn encode_tiled()
 
 // 2-D map over a row-major [rows, cols] tensor; box = [box_rows][128 bytes], 128-byte swizzle,
 // out-of-range rows read as zero
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int es, int box_rows)
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int es, int box_rows, int64_t ld = 0)
 {
     EncodeTiledFn fn = encode_tiled();
     if (!fn) return false;
+    if (!ld) ld = cols * es;  // row pitch in bytes
     const CUtensorMapDataType dt = es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : (es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * (cuuint64_t)es};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld};
     const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
     return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -470,6 +472,11 @@ bool tensor_map_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
     return make_map(m, base, rows, cols, es, box_rows);
 }
 bool device_of(const void* p) { return use_device_of(p); }
+
+bool tensor_map_bytes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows)
+{
+    return make_map(m, base, rows, cols, 1, box_rows, ld);
+}
 size_t encode_workspace_bytes(int64_t rows, int64_t cols, int32_t n, int src)
 {
     return valid_tile(n) ? ws_bytes_for_src(rows, cols, n, src) : 0;
@@ -873,6 +880,16 @@ hq_status_t hq_status_read(const void* ws, void* stream, int64_t* detail)
     if (cudaStreamSynchronize(st) != cudaSuccess) return HQ_ERR_CUDA;
     WsHeader h;
     if (cudaMemcpy(&h, ws, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return HQ_ERR_CUDA;
+    if (h.slots > 0 && h.slots <= (uint32_t)kMaxSlots) {  // one status per block: merge them
+        StatusSlot s[kMaxSlots];
+        if (cudaMemcpy(s, static_cast<const char*>(ws) + sizeof(h), h.slots * sizeof(StatusSlot),
+                       cudaMemcpyDeviceToHost) != cudaSuccess)
+            return HQ_ERR_CUDA;
+        for (uint32_t i = 0; i < h.slots; ++i) {
+            h.status |= s[i].status;
+            h.nonfinite += s[i].nonfinite;
+        }
+    }
     const hq_status_t order[] = {HQ_ERR_TIMEOUT, HQ_ERR_CORRUPT, HQ_ERR_CAPACITY, HQ_ERR_RANGE, HQ_ERR_NONFINITE};
     for (hq_status_t s : order) {
         if (h.status & (1u << s)) {

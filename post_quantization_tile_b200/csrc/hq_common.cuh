@@ -37,13 +37,14 @@ constexpr uint32_t kStTimeout = 1u << HQ_ERR_TIMEOUT;
 constexpr uint32_t kStRange = 1u << HQ_ERR_RANGE;
 
 // Workspace layout (bytes): [0] status u32, [4] nonfinite tiles u32, [8] words needed u64,
-// [16] work counter u32, [24] count-only total u64, [64 ..] look-back states u64 per item.
+// [16] work counter u32, [20] number of status slots u32 (8-bit operators: one per block, behind the
+// header), [24] count-only total u64, [64 ..] look-back states u64 per item.
 struct WsHeader {
     uint32_t status;
     uint32_t nonfinite;
     unsigned long long needed;
     uint32_t counter;
-    uint32_t pad0;
+    uint32_t slots;
     unsigned long long count_bits;
     uint32_t pad1[8];
 };

@@ -1,0 +1,116 @@
+// hq_fp8.cuh -- helpers shared by the 8-bit floating-point kernels: e4m3 conversions, the
+// power-of-two scale of a block, and the status slots of the workspace.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "hq_common.cuh"
+
+namespace hq {
+
+// ------------------------------------------------------------------------------------------------
+// Status without a clearing launch: every block of a grid owns one slot and writes it in any case;
+// block 0 writes the header with their number, and hq_status_read merges them.  `ws` may be NULL
+// (nothing is recorded then).  The grids are at most kMaxSlots blocks (each walks its share).
+// ------------------------------------------------------------------------------------------------
+struct StatusSlot {
+    uint32_t status;
+    uint32_t nonfinite;
+};
+constexpr int kMaxSlots = 4096;
+constexpr size_t kSlotBytes = sizeof(WsHeader) + sizeof(StatusSlot) * kMaxSlots;
+
+__device__ __forceinline__ void slot_write(WsHeader* ws, uint32_t slots, uint32_t slot, uint32_t status, uint32_t nonfinite)
+{
+    if (!ws) return;
+    StatusSlot* s = reinterpret_cast<StatusSlot*>(ws + 1);
+    s[slot] = StatusSlot{status, nonfinite};
+    if (slot == 0) {
+        WsHeader h{};
+        h.slots = slots;
+        *ws = h;
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// e4m3
+// ------------------------------------------------------------------------------------------------
+// two binary32 -> two e4m3 codes (lo in the low byte), nearest even, saturating at 448
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// two e4m3 codes (the low 16 bits of w) -> binary16 pair, exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+    return r;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w)
+{
+    const uint32_t h = e4m3x2_to_f16x2(w);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// the four codes of w times r (a power of two unless the scales came from elsewhere), coded again
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float r)
+{
+    const float2 a = e4m3x2_to_float2(w & 0xFFFFu), b = e4m3x2_to_float2(w >> 16);
+    return e4m3x4(__fmul_rn(a.x, r), __fmul_rn(a.y, r), __fmul_rn(b.x, r), __fmul_rn(b.y, r));
+}
+
+// Exponent e of a block's scale 2^e from the bit pattern of its largest magnitude: the smallest e
+// in [-40, 40] with amax <= 448 * 2^e (448 = 1.75 * 2^8, the largest e4m3 number).  A power of two
+// costs e4m3 nothing but the place of its subnormals, and makes x / 2^e, and the codes of a block
+// whose scale grows, exact.  The range keeps the ratio of any two scales inside binary32.
+constexpr int kScaleExpMin = -40, kScaleExpMax = 40;
+__device__ __forceinline__ int scale_exp(uint32_t amax_bits)
+{
+    const int e = (int)(amax_bits >> 23) - 127 - ((amax_bits & 0x7FFFFFu) <= 0x600000u ? 8 : 7);
+    return max(kScaleExpMin, min(kScaleExpMax, e));
+}
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + e) << 23); }
+// the largest magnitude the largest scale can hold (448 * 2^40), as a bit pattern
+constexpr uint32_t kAmaxLimit = ((127u + 48u) << 23) | 0x600000u;
+
+// eight elements from 16-byte aligned memory as binary32
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8])
+{
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    v[0] = bf16lo_to_f32(w.x), v[1] = bf16hi_to_f32(w.x), v[2] = bf16lo_to_f32(w.y), v[3] = bf16hi_to_f32(w.y);
+    v[4] = bf16lo_to_f32(w.z), v[5] = bf16hi_to_f32(w.z), v[6] = bf16lo_to_f32(w.w), v[7] = bf16hi_to_f32(w.w);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+
+// largest bit pattern of |v|: above 0x7F7FFFFF where an element is infinite or NaN
+__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+constexpr uint32_t kFiniteMax = 0x7F7FFFFFu;
+
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv)
+{
+    uint2 w;
+    w.x = e4m3x4(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv), __fmul_rn(v[2], inv), __fmul_rn(v[3], inv));
+    w.y = e4m3x4(__fmul_rn(v[4], inv), __fmul_rn(v[5], inv), __fmul_rn(v[6], inv), __fmul_rn(v[7], inv));
+    return w;
+}
+
+}  // namespace hq

@@ -1,0 +1,266 @@
+// hq_gemm_fp8.cu -- e4m3 tensor-core GEMM with a scale for each block of 128 (tcgen05 MMA, TMEM
+// accumulators, TMA operand loads).
+//
+//   Y[m, n] = sum_t sa[t, m] sw[t, n / 128] S_{m,n,t},  S_{m,n,t} = sum_{k in block t} A[m, k] W[n, k]
+//
+// A [M, K] carries one scale per row and 128 columns, W [N, K] one per 128 x 128 block.  A block's sum
+// S is one accumulation of four MMAs (K = 32 each) in TMEM; the scales differ from block to block,
+// so the epilogue warps take every block's sums out and add them, scaled, in binary32 registers:
+// acc = fma(S, sa sw, acc) over t in order.
+//
+// Persistent CTAs (one per SM) walk the 128 x GN tiles of Y (GN = 128 columns; 64 or 32 where the
+// 128-wide tiles are too few to occupy the SMs): warp 0 streams 128-byte wide boxes of A and W into a
+// ring with TMA (128-byte swizzle; rows and columns outside the matrices read as zeros), warp 1
+// issues the MMAs of a block into one of 512 / GN accumulator slots, the epilogue warps (warpgroups of
+// 32 columns each) read each finished slot, release it and scale.  Every wait is bounded: on a
+// timeout the kernel records HQ_ERR_TIMEOUT and winds down.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "hq_fp8.cuh"
+#include "hq_launch.h"
+#include "hq_tc.cuh"
+
+namespace hq {
+namespace {
+
+constexpr int GM = 128, GK = 128;  // CTA tile rows and K block
+
+template <int GN>
+struct F8Cfg {
+    static constexpr int STAGES = GN == 128 ? 6 : 8;  // operand ring
+    static constexpr int ACC = 512 / GN;              // accumulator slots
+    static constexpr int EPI = GN / 8;                // epilogue warps: GN / 32 warpgroups of 32 columns
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr uint32_t IDESC = idesc_f8(GM, GN);
+};
+
+template <int GN>
+struct F8Smem {
+    using C = F8Cfg<GN>;
+    alignas(1024) uint8_t a[C::STAGES][GM * GK];
+    alignas(1024) uint8_t b[C::STAGES][GN * GK];
+    alignas(8) uint64_t full[C::STAGES];
+    uint64_t empty[C::STAGES];
+    uint64_t acc_full[C::ACC];
+    uint64_t acc_empty[C::ACC];
+    uint32_t tmem_base;
+    uint32_t status;
+};
+
+struct F8Args {
+    int64_t M, N, K;
+    const float* sa;
+    const float* sw;
+    void* Y;
+    int bf16, vec;
+    WsHeader* ws;
+};
+
+template <int GN>
+__global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
+    gemm_fp8_kernel(const F8Args a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB)
+{
+    using C = F8Cfg<GN>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    F8Smem<GN>& sm = *reinterpret_cast<F8Smem<GN>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int KB = (int)((a.K + GK - 1) / GK);
+    const int NT = (int)((a.N + GN - 1) / GN);
+    const int64_t tiles = ((a.M + GM - 1) / GM) * NT;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int s = 0; s < C::ACC; ++s) {
+            mbar_init(&sm.acc_full[s], 1);
+            mbar_init(&sm.acc_empty[s], C::EPI);
+        }
+        sm.status = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = sm.tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool alive = true;
+            for (int64_t tile = blockIdx.x; alive && tile < tiles; tile += gridDim.x) {
+                const int m0 = (int)(tile / NT) * GM, n0 = (int)(tile % NT) * GN;
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const int s = it % C::STAGES;
+                    if (it >= C::STAGES && !mbar_wait_sleep(&sm.empty[s], (uint32_t)((it / C::STAGES - 1) & 1))) {
+                        atomicOr(&sm.status, kStTimeout);
+                        alive = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(GM * GK + GN * GK));
+                    tma_load_2d(sm.a[s], &tA, kb * GK, m0, &sm.full[s]);
+                    tma_load_2d(sm.b[s], &tB, kb * GK, n0, &sm.full[s]);
+                }
+            }
+            // no copy may be in flight when the block leaves: wait for the last boxes
+            for (int j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j)
+                mbar_wait_sleep(&sm.full[j % C::STAGES], (uint32_t)((j / C::STAGES) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0;
+            bool alive = true;
+            for (int64_t tile = blockIdx.x; alive && tile < tiles; tile += gridDim.x) {
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const int s = it % C::STAGES, slot = it % C::ACC;
+                    if ((it >= C::ACC && !mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / C::ACC - 1) & 1))) ||
+                        !mbar_wait_sleep(&sm.full[s], (uint32_t)((it / C::STAGES) & 1))) {
+                        atomicOr(&sm.status, kStTimeout);
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = sw128_desc(sm.a[s]), bd = sw128_desc(sm.b[s]);
+#pragma unroll
+                    for (int kk = 0; kk < GK / 32; ++kk)  // K 32 per MMA: the start address moves 32 bytes
+                        mma_f8(tbase + (uint32_t)(slot * GN), ad + (uint64_t)(2 * kk), bd + (uint64_t)(2 * kk), C::IDESC,
+                               kk > 0 ? 1u : 0u);
+                    mma_commit(&sm.empty[s]);
+                    mma_commit(&sm.acc_full[slot]);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // warpgroup h takes columns 32 h .. 32 h + 31 of each slot; a warp reads the TMEM lane quarter
+        // warp % 4, one row of the tile per thread
+        const int q = warp & 3, h = (warp - 2) >> 2, row = q * 32 + lane;
+        const int64_t NB = (a.N + 127) / 128;
+        int it = 0;
+        bool alive = true;
+        for (int64_t tile = blockIdx.x; alive && tile < tiles; tile += gridDim.x) {
+            const int64_t m = (tile / NT) * GM + row, n0 = (tile % NT) * GN + 32 * h;
+            const float* sa = a.sa + (m < a.M ? m : 0);
+            const float* sw = a.sw + n0 / 128;
+            const bool some = n0 < a.N;  // the last tile's warpgroups may lie past N
+            float2 acc[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            float f = some ? __ldg(sa) * __ldg(sw) : 0.0f;
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int slot = it % C::ACC;
+                // the next block's scales are on their way while this block's sums are awaited
+                const float nsa = some && kb + 1 < KB ? __ldg(sa + (int64_t)(kb + 1) * a.M) : 0.0f;
+                const float nsw = some && kb + 1 < KB ? __ldg(sw + (int64_t)(kb + 1) * NB) : 0.0f;
+                const bool got = mbar_wait_sleep(&sm.acc_full[slot], (uint32_t)((it / C::ACC) & 1));
+                __syncwarp();
+                if (!__all_sync(0xFFFFFFFFu, got)) {
+                    if (lane == 0) atomicOr(&sm.status, kStTimeout);
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t S[32];
+                tmem_ld32_nowait(tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * GN + 32 * h), S);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.acc_empty[slot]);
+                const float2 ff = make_float2(f, f);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    acc[c] = __ffma2_rn(make_float2(__uint_as_float(S[2 * c]), __uint_as_float(S[2 * c + 1])), ff, acc[c]);
+                f = nsa * nsw;
+            }
+            if (!alive || m >= a.M || !some) continue;
+            const int left = (int)(a.N - n0 < 32 ? a.N - n0 : 32);
+            if (a.bf16) {
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + m * a.N + n0;
+                if (a.vec && left == 32) {
+#pragma unroll
+                    for (int c = 0; c < 16; c += 4) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c + j].x, acc[c + j].y);
+                            w[j] = *reinterpret_cast<const uint32_t*>(&x);
+                        }
+                        *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        if (2 * c < left) y[2 * c] = __float2bfloat16_rn(acc[c].x);
+                        if (2 * c + 1 < left) y[2 * c + 1] = __float2bfloat16_rn(acc[c].y);
+                    }
+                }
+            } else {
+                float* y = static_cast<float*>(a.Y) + m * a.N + n0;
+                if (a.vec && left == 32) {
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2)
+                        *reinterpret_cast<float4*>(y + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        if (2 * c < left) y[2 * c] = acc[c].x;
+                        if (2 * c + 1 < left) y[2 * c + 1] = acc[c].y;
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tbase, 512);
+    if (threadIdx.x == 0) slot_write(a.ws, gridDim.x, blockIdx.x, sm.status, 0u);
+}
+
+template <int GN>
+cudaError_t launch_gemm_fp8(const F8Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st)
+{
+    const size_t smem = sizeof(F8Smem<GN>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_kernel<GN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ((a.M + GM - 1) / GM) * ((a.N + GN - 1) / GN);
+    const int grid = (int)(tiles < num_sms() ? tiles : num_sms());
+    gemm_fp8_kernel<GN><<<grid, F8Cfg<GN>::THREADS, smem, st>>>(a, ta, tb);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace hq
+
+using namespace hq;
+
+extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W, int64_t ldw,
+                                   const float* sw, int64_t N, int64_t K, void* Y, hq_dtype_t ydtype, void* ws,
+                                   size_t ws_bytes, void* stream)
+{
+    if (!A || !sa || !W || !sw || !Y || M < 1 || N < 1 || K < 1 || lda < K || ldw < K || lda % 16 || ldw % 16) return HQ_ERR_ARG;
+    if (ydtype != HQ_BF16 && ydtype != HQ_F32) return HQ_ERR_ARG;
+    if (M > ((int64_t)1 << 30) || N > ((int64_t)1 << 30) || K > ((int64_t)1 << 20)) return HQ_ERR_UNSUPPORTED;
+    const uintptr_t es = ydtype == HQ_BF16 ? 2 : 4, y = reinterpret_cast<uintptr_t>(Y);
+    if ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(W)) & 15u) return HQ_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(sa) | reinterpret_cast<uintptr_t>(sw)) & 3u || y % es) return HQ_ERR_ARG;
+    if (ws && (ws_bytes < kSlotBytes || (reinterpret_cast<uintptr_t>(ws) & 15u))) return HQ_ERR_ARG;
+    DeviceGuard dev(A);
+    if (!dev.ok) return HQ_ERR_ARG;
+    const int64_t sms = num_sms(), mt = (M + GM - 1) / GM;
+    int gn = 128;  // the widest tile whose tiles occupy every SM, 32 columns if none does
+    while (gn > 32 && mt * ((N + gn - 1) / gn) < sms) gn /= 2;
+    // K blocks over all tiles of a CTA are counted in 31 bits
+    if ((mt * ((N + gn - 1) / gn) / sms + 1) * ((K + GK - 1) / GK) > ((int64_t)1 << 30)) return HQ_ERR_UNSUPPORTED;
+    CUtensorMap ta, tb;
+    if (!tensor_map_bytes(&ta, A, M, K, lda, GM) || !tensor_map_bytes(&tb, W, N, K, ldw, gn)) return HQ_ERR_CUDA;
+    F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, static_cast<WsHeader*>(ws)};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = gn == 128 ? launch_gemm_fp8<128>(a, ta, tb, st)
+                                    : (gn == 64 ? launch_gemm_fp8<64>(a, ta, tb, st) : launch_gemm_fp8<32>(a, ta, tb, st));
+    return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+}

@@ -1,0 +1,659 @@
+// hq_kv8_attend.cu -- attention of bf16 queries over the e4m3 KV cache.
+//
+//   s_rj = scale q_r . k_j,  out_r = sum_j exp(s_rj) v_j / sum_j exp(s_rj) over the visible slots j
+//
+// One pass over the keys and values with a running maximum and sum.  The rows r of one (sequence,
+// key head) are its queries times the query heads of the group; sixteen of them make one unit, and
+// all of them share the keys and values that a warp loads.  The units' tokens, in tiles of 64, are
+// laid end to end and cut into equal shares, one per resident thread block, so ragged batches and
+// single long sequences fill the GPU alike; where a unit is cut, the parts leave their maximum, sum and
+// accumulator in the workspace and a second small kernel joins them.
+//
+// Codes become binary16 in registers (one conversion instruction for two codes, exact) and both
+// products run on the matrix instruction m16n8k16 with binary32 accumulators.  The order of the
+// contraction and of the output columns is free, so every lane loads 16 contiguous bytes of a key or
+// value row straight from global memory into the places its fragments need: no shared memory and
+// no transposition but byte pairs of two value rows.
+//   - queries become binary16 after a power-of-two scaling per row (bf16's 8 bits fit exactly, elements
+//     below 2^-38 of the row's largest lose bits);
+//   - probabilities become binary16 at 2^10 times their value relative to the running maximum: 11
+//     bits, and weights down to 2^-34 of the largest still count;
+//   - key scales multiply the scores, value scales stay out of the products: the accumulator is kept in
+//     units of the last value scale and multiplied by the (power-of-two) ratio when that changes.
+#include <cuda_runtime.h>
+
+#include "hq_kv8.cuh"
+
+namespace hq {
+namespace {
+
+constexpr int kWarps = 4, kThreadsA = 32 * kWarps;
+constexpr int kTile = 64;         // tokens of one share unit
+constexpr int kMaxBatch = 4096;   // sequences of one call (their prefix sums live in shared memory)
+constexpr int kMaxGrid = 512;
+constexpr float kBoost = 10.0f;   // probabilities are held times 2^10
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttendArgs {
+    hq_kv8_t c;
+    const __nv_bfloat16* q;
+    int64_t qb, qh, qs;
+    __nv_bfloat16* out;
+    int64_t ob, oh, os;
+    int B, Hq, Sq, G, page_shift;
+    const int32_t* table;
+    int64_t table_stride;
+    int64_t slots;  // max_pages * page
+    const int32_t* lens;
+    const int32_t* q_lens;
+    float scale;
+    int causal;
+    float* lse;
+    int64_t lb, lh;
+    const float* win;
+    float* w;
+    int64_t wib, wih, wb, wh, L;
+    uint32_t* prefix;  // [B + 1] share units before each sequence
+    float* part_o;     // [2 grid][16][D]
+    float2* part_ml;   // [2 grid][16]
+    float* lse2;       // [B][heads][G Sq] binary logarithm of the sums (weights only)
+    WsHeader* ws;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// lengths of sequence b: cached slots and queries, inside what the call's shapes allow
+struct SeqLen {
+    int n, m;
+    bool odd;
+};
+__device__ __forceinline__ SeqLen seq_len(const AttendArgs& a, int b)
+{
+    SeqLen s;
+    const int n = a.lens[b], m = a.q_lens ? a.q_lens[b] : a.Sq;
+    s.n = (int)max((int64_t)0, min((int64_t)n, a.slots));
+    s.m = max(0, min(m, a.Sq));
+    s.odd = n != s.n || m != s.m || (a.w && s.n > a.L);
+    return s;
+}
+__device__ __forceinline__ int row_tiles(const AttendArgs& a, int m) { return (m * a.G + 15) / 16; }
+// slots that query i of m sees, of n
+__device__ __forceinline__ int sees(const AttendArgs& a, int n, int m, int i)
+{
+    return a.causal ? max(0, n - m + i + 1) : n;
+}
+
+// sixteen query rows as the A fragments of the score product, and the factors of their scores
+template <int D>
+struct QueryRows {
+    uint32_t f[D / 16][4];
+    float c[2];  // score factor of rows lane / 4 and lane / 4 + 8
+    int end[2];  // slots they see (0: no such row)
+
+    __device__ __forceinline__ void load(const AttendArgs& a, int b, int h, int rt, const SeqLen& s)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int r = rt * 16 + g + 8 * half, i = r / a.G;
+            const bool is = i < s.m;
+            const __nv_bfloat16* q = a.q + b * a.qb + (int64_t)(h * a.G + (is ? r - i * a.G : 0)) * a.qh + (is ? i : 0) * a.qs;
+            uint2 w[D / 16];
+            uint32_t m = 0;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                w[kk] = is ? __ldg(reinterpret_cast<const uint2*>(q + (kk >> 2) * 64 + t * 16 + (kk & 3) * 4)) : make_uint2(0u, 0u);
+                m = max(m, max(max((w[kk].x << 16) & 0x7FFF0000u, w[kk].x & 0x7FFF0000u),
+                               max((w[kk].y << 16) & 0x7FFF0000u, w[kk].y & 0x7FFF0000u)));
+            }
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            const int e = m ? min(126, 14 + 127 - (int)(m >> 23)) : 0;
+            const float up = exp2_int(e);
+            c[half] = exp2_int(-e) * a.scale * kLog2e;
+            end[half] = is ? sees(a, s.n, s.m, i) : 0;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                f[kk][half] = pack_f16(bf16lo_to_f32(w[kk].x) * up, bf16hi_to_f32(w[kk].x) * up);
+                f[kk][half + 2] = pack_f16(bf16lo_to_f32(w[kk].y) * up, bf16hi_to_f32(w[kk].y) * up);
+            }
+        }
+    }
+};
+
+// sixteen tokens' keys: lane (g, t) holds 16-byte runs of the two tokens whose scores are the columns g
+// of its two score tiles
+template <int D>
+struct KeyGroup {
+    uint4 w[2][D / 64];
+
+    __device__ __forceinline__ void load(const uint8_t* k, bool ok)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+                w[i][j] = ok ? __ldg(reinterpret_cast<const uint4*>(k + (4 * (g >> 1) + (g & 1) + 2 * i) * D + j * 64 + t * 16))
+                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void scores(const QueryRows<D>& q, float (&s)[2][4]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const uint32_t x[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    mma16816(s[i], q.f[4 * j + y], e4m3x2_to_f16x2(x[y] & 0xFFFFu), e4m3x2_to_f16x2(x[y] >> 16));
+            }
+        }
+    }
+};
+
+// sixteen tokens' values: lane (g, t) holds dims g D/8 .. of tokens 4 t .. 4 t + 3
+template <int D>
+struct ValueGroup {
+    uint32_t w[4][D / 32];
+
+    __device__ __forceinline__ void load(const uint8_t* v, bool ok, int left)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t* at = v + (4 * t + i) * D + g * (D / 8);
+            const bool is = ok && 4 * t + i < left;  // slots nobody sees may hold anything: zero times NaN
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) w[i][j] = 0u;
+            if (is) {
+                if (D == 128) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+                    w[i][0] = x.x, w[i][1] = x.y, w[i][D / 32 - 2] = x.z, w[i][D / 32 - 1] = x.w;
+                } else {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+                    w[i][0] = x.x, w[i][1] = x.y;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void accumulate(const uint32_t (&p)[4], float (&o)[D / 8][4]) const
+    {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            const uint32_t lo0 = __byte_perm(w[0][j], w[1][j], 0x5140), hi0 = __byte_perm(w[0][j], w[1][j], 0x7362);
+            const uint32_t lo1 = __byte_perm(w[2][j], w[3][j], 0x5140), hi1 = __byte_perm(w[2][j], w[3][j], 0x7362);
+            mma16816(o[4 * j], p, e4m3x2_to_f16x2(lo0 & 0xFFFFu), e4m3x2_to_f16x2(lo1 & 0xFFFFu));
+            mma16816(o[4 * j + 1], p, e4m3x2_to_f16x2(lo0 >> 16), e4m3x2_to_f16x2(lo1 >> 16));
+            mma16816(o[4 * j + 2], p, e4m3x2_to_f16x2(hi0 & 0xFFFFu), e4m3x2_to_f16x2(hi1 & 0xFFFFu));
+            mma16816(o[4 * j + 3], p, e4m3x2_to_f16x2(hi0 >> 16), e4m3x2_to_f16x2(hi1 >> 16));
+        }
+    }
+};
+
+// where sixteen tokens from slot `tok` lie; false if their page is outside the pool
+__device__ __forceinline__ bool locate(const AttendArgs& a, const int32_t* table, int h, int tok, int64_t& ph, int64_t& row)
+{
+    const int32_t id = __ldg(table + (tok >> a.page_shift));
+    const bool ok = id >= 0 && id < a.c.pages;
+    ph = ok ? (int64_t)id * a.c.heads + h : 0;
+    row = (ph << a.page_shift) + (tok & (a.c.page - 1));
+    return ok;
+}
+
+template <int D>
+struct AttendSmem {
+    float o[kWarps][16][D + 4];
+    float m[kWarps][16], l[kWarps][16];
+    uint32_t scan[kWarps];
+    uint32_t status;
+};
+
+// a finished row r of a unit: the output, the logarithm of its sum
+__device__ __forceinline__ void row_place(const AttendArgs& a, int h, int r, int& head, int& i)
+{
+    i = r / a.G;
+    head = h * a.G + (r - i * a.G);
+}
+__device__ __forceinline__ void write_lse(const AttendArgs& a, int b, int h, int r, float M, float l)
+{
+    int head, i;
+    row_place(a, h, r, head, i);
+    const float l2 = l > 0.0f ? M - kBoost + log2f(l) : (l == 0.0f ? -INFINITY : l);  // a NaN sum stays one
+    if (a.lse) a.lse[b * a.lb + head * a.lh + i] = l2 * kLn2;
+    if (a.lse2) a.lse2[((int64_t)b * a.c.heads + h) * a.G * a.Sq + r] = l2;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsA, 2) kv8_attend_kernel(const AttendArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    AttendSmem<D>& sm = *reinterpret_cast<AttendSmem<D>*>(smem_raw);
+    uint32_t* pre = reinterpret_cast<uint32_t*>(smem_raw + sizeof(AttendSmem<D>));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    if (tid == 0) sm.status = 0u;
+    // prefix sums of the sequences' share units
+    {
+        const int run = (a.B + kThreadsA - 1) / kThreadsA, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+        uint32_t mine = 0;
+        bool odd = false;
+        for (int b = b0; b < b1; ++b) {
+            const SeqLen s = seq_len(a, b);
+            odd |= s.odd;
+            mine += (uint32_t)(a.c.heads * row_tiles(a, s.m)) * (uint32_t)((s.n + kTile - 1) / kTile);
+        }
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        if (lane == 31) sm.scan[warp] = inc;
+        __syncthreads();
+        uint32_t at = inc - mine;
+        for (int i = 0; i < warp; ++i) at += sm.scan[i];
+        for (int b = b0; b < b1; ++b) {
+            pre[b] = at;
+            const SeqLen s = seq_len(a, b);
+            at += (uint32_t)(a.c.heads * row_tiles(a, s.m)) * (uint32_t)((s.n + kTile - 1) / kTile);
+        }
+        if (tid == kThreadsA - 1) pre[a.B] = at;
+        if (odd && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int b = tid; b <= a.B; b += kThreadsA) a.prefix[b] = pre[b];
+    }
+    const uint32_t W = pre[a.B];
+    const uint32_t shares = min(W, gridDim.x);  // none is empty: the join walks a unit's shares one by one
+    uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
+    const uint32_t w1 = blockIdx.x < shares ? (uint32_t)((uint64_t)(blockIdx.x + 1) * W / shares) : 0u;
+    bool bad = false;
+    while (w0 < w1) {
+        // the unit that share unit w0 belongs to
+        int b = 0;
+        for (int hi = a.B; hi - b > 1;) {
+            const int mid = (b + hi) >> 1;
+            if (pre[mid] <= w0) b = mid;
+            else hi = mid;
+        }
+        const SeqLen s = seq_len(a, b);
+        const uint32_t tiles = (uint32_t)((s.n + kTile - 1) / kTile);
+        const int rts = row_tiles(a, s.m);
+        const uint32_t unit = (w0 - pre[b]) / tiles, t0 = (w0 - pre[b]) % tiles;
+        const uint32_t t1 = min(tiles, t0 + (w1 - w0));
+        const int h = unit / rts, rt = unit % rts;
+        const int last_row = min(rt * 16 + 15, s.m * a.G - 1);
+        const int end = min((int)t1 * kTile, sees(a, s.n, s.m, last_row / a.G));
+        const int groups = (end + 15) / 16;  // sixteen-token groups up to the last visible slot
+        const int32_t* table = a.table + b * a.table_stride;
+
+        QueryRows<D> q;
+        q.load(a, b, h, rt, s);
+        float o[D / 8][4];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vref = 1.0f;
+
+        for (int gr = (int)t0 * (kTile / 16) + warp; gr < groups; gr += kWarps) {
+            const int tok = gr * 16;
+            int64_t ph, row;
+            const bool ok = locate(a, table, h, tok, ph, row);
+            bad |= !ok;
+            KeyGroup<D> k;
+            ValueGroup<D> v;
+            k.load(a.c.k + row * D, ok);
+            v.load(a.c.v + row * D, ok, end - tok);
+            const float ks = __ldg(a.c.k_scale + ph), vs = ok ? __ldg(a.c.v_scale + ph) : vref;
+            float x[2][4];
+            k.scores(q, x);
+            float top[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float c = q.c[half] * ks;
+                const int left = ok ? q.end[half] - tok : 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        x[i][2 * half + e] = 4 * t + 2 * i + e < left ? x[i][2 * half + e] * c : -INFINITY;
+                top[half] = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
+                top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
+                top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 2));
+                top[half] = fmaxf(top[half], m[half]);
+            }
+            // a changed maximum or value scale changes the accumulator's units
+            const float vr = vref / vs;
+            if (__any_sync(0xFFFFFFFFu, top[0] != m[0] || top[1] != m[1] || vr != 1.0f)) {
+                float f[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    f[half] = m[half] == -INFINITY ? 1.0f : ex2(m[half] - top[half]);
+                    l[half] *= f[half];
+                    f[half] *= vr;
+                    m[half] = top[half];
+                }
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][0] *= f[0];
+                    o[j][1] *= f[0];
+                    o[j][2] *= f[1];
+                    o[j][3] *= f[1];
+                }
+                vref = vs;
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float sub = m[half] == -INFINITY ? 0.0f : m[half] - kBoost;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[i][2 * half + e] = ex2(x[i][2 * half + e] - sub);
+                        l[half] += x[i][2 * half + e];
+                    }
+            }
+            const uint32_t p[4] = {pack_f16(x[0][0], x[0][1]), pack_f16(x[0][2], x[0][3]), pack_f16(x[1][0], x[1][1]),
+                                   pack_f16(x[1][2], x[1][3])};
+            v.accumulate(p, o);
+        }
+
+        // join the warps: their accumulators through shared memory, each at the common maximum
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 1);
+            l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 2);
+            if (t == 0) {
+                sm.m[warp][g + 8 * half] = m[half];
+                sm.l[warp][g + 8 * half] = l[half];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < D / 8; j += 4)
+                    *reinterpret_cast<float4*>(&sm.o[warp][g + 8 * half][(2 * t + e) * (D / 8) + j]) =
+                        make_float4(o[j][2 * half + e] * vref, o[j + 1][2 * half + e] * vref, o[j + 2][2 * half + e] * vref,
+                                    o[j + 3][2 * half + e] * vref);
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == tiles;
+        const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+        constexpr int TPR = kThreadsA / 16, DPT = D / TPR;  // threads of a row, dims of a thread
+        const int r = tid / TPR, d0 = (tid % TPR) * DPT;
+        float M = -INFINITY, f[kWarps], L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.m[w][r]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            f[w] = sm.m[w][r] == -INFINITY ? 1.0f : ex2(sm.m[w][r] - M);
+            L += sm.l[w][r] * f[w];
+        }
+        const int rr = rt * 16 + r;
+        if (!whole || rr < s.m * a.G) {
+            const float inv = whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
+            int head, i;
+            row_place(a, h, rr, head, i);
+            __nv_bfloat16* out = a.out + b * a.ob + head * a.oh + (int64_t)i * a.os;
+            if (d0 == 0) {
+                if (whole) write_lse(a, b, h, rr, M, L);
+                else a.part_ml[slot * 16 + r] = make_float2(M, L);
+            }
+#pragma unroll
+            for (int d = 0; d < DPT; d += 4) {
+                float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][d0 + d]);
+                    y.x = fmaf(x.x, f[w], y.x), y.y = fmaf(x.y, f[w], y.y), y.z = fmaf(x.z, f[w], y.z), y.w = fmaf(x.w, f[w], y.w);
+                }
+                if (whole) {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * inv, y.y * inv), hi = __floats2bfloat162_rn(y.z * inv, y.w * inv);
+                    *reinterpret_cast<uint2*>(out + d0 + d) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                } else {
+                    *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * 16 + r) * D + d0 + d) = y;
+                }
+            }
+        }
+        __syncthreads();
+        w0 += t1 - t0;
+    }
+    if (bad) atomicOr(&sm.status, kStRange);
+    __syncthreads();
+    if (tid == 0) slot_write(a.ws, gridDim.x, blockIdx.x, sm.status, 0u);
+}
+
+// joins the parts of the units that were cut, and writes zeros where a row sees nothing
+template <int D>
+__global__ void __launch_bounds__(128) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
+{
+    const int rt = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
+    const int h = bh % a.c.heads, b = bh / a.c.heads;
+    const SeqLen s = seq_len(a, b);
+    const int rts = row_tiles(a, s.m);
+    if (rt >= rts) return;
+    const uint32_t tiles = (uint32_t)((s.n + kTile - 1) / kTile), W = a.prefix[a.B];
+    const uint32_t w0 = a.prefix[b] + ((uint32_t)h * rts + rt) * tiles, w1 = w0 + tiles;
+    // the share that holds share unit w: the smallest c with w < floor((c + 1) W / shares)
+    const uint32_t shares = min(W, (uint32_t)grid);
+    const int c0 = tiles ? (int)(((uint64_t)(w0 + 1) * shares - 1) / W) : 0;
+    const int c1 = tiles ? (int)(((uint64_t)w1 * shares - 1) / W) : 0;
+    if (tiles && c0 == c1) return;  // whole: written already
+    constexpr int TPR = 8, DPT = D / TPR;
+    const int r = threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * DPT, rr = rt * 16 + r;
+    if (rr >= s.m * a.G) return;
+    float M = -INFINITY, L = 0.0f, y[DPT];
+#pragma unroll
+    for (int d = 0; d < DPT; ++d) y[d] = 0.0f;
+    if (tiles) {
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * c + (c == c0)) * 16 + r].x);
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t at = (int64_t)(2 * c + (c == c0)) * 16 + r;
+            const float2 ml = a.part_ml[at];
+            const float f = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
+            L = fmaf(ml.y, f, L);
+#pragma unroll
+            for (int d = 0; d < DPT; d += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + d0 + d);
+                y[d] = fmaf(x.x, f, y[d]), y[d + 1] = fmaf(x.y, f, y[d + 1]), y[d + 2] = fmaf(x.z, f, y[d + 2]), y[d + 3] = fmaf(x.w, f, y[d + 3]);
+            }
+        }
+    }
+    if (d0 == 0) write_lse(a, b, h, rr, M, L);
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    int head, i;
+    row_place(a, h, rr, head, i);
+    __nv_bfloat16* out = a.out + b * a.ob + head * a.oh + (int64_t)i * a.os + d0;
+#pragma unroll
+    for (int d = 0; d < DPT; d += 2) *reinterpret_cast<__nv_bfloat162*>(out + d) = __floats2bfloat162_rn(y[d] * inv, y[d + 1] * inv);
+}
+
+// The weight each cached slot received, summed over a key head's rows: with the rows' sums known,
+// exp(s - lse) is recomputed from the keys.  One warp takes sixteen slots and walks the row tiles, so
+// every slot is summed by one lane group in a fixed order.
+template <int D>
+__global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendArgs a)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const SeqLen s = seq_len(a, b);
+    const int n = (int)min((int64_t)s.n, a.L);
+    const int tok = (blockIdx.x * kWarps + warp) * 16;
+    if (tok >= n) return;
+    int64_t ph, row;
+    const bool ok = locate(a, a.table + b * a.table_stride, h, tok, ph, row);
+    KeyGroup<D> k;
+    k.load(a.c.k + row * D, ok);
+    const float ks = __ldg(a.c.k_scale + ph);
+    float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+    const float* lse2 = a.lse2 + ((int64_t)b * a.c.heads + h) * a.G * a.Sq;
+    const int rts = row_tiles(a, s.m);
+    for (int rt = 0; rt < rts; ++rt) {
+        QueryRows<D> q;
+        q.load(a, b, h, rt, s);
+        float x[2][4];
+        k.scores(q, x);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float c = q.c[half] * ks;
+            const int r = rt * 16 + g + 8 * half, left = ok ? q.end[half] - tok : 0;
+            const float l2 = r < s.m * a.G ? lse2[r] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (4 * t + 2 * i + e < left) sum[i][e] += ex2(x[i][2 * half + e] * c - l2);
+        }
+    }
+    const float* win = a.win ? a.win + b * a.wib + h * a.wih : nullptr;
+    float* w = a.w + b * a.wb + h * a.wh;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x = sum[i][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+            const int j = tok + 4 * t + 2 * i + e;
+            if (g == 0 && j < n) w[j] = win ? win[j] + x : x;
+        }
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct AttendLayout {
+    size_t prefix, part_o, part_ml, lse2, bytes;
+};
+AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool weights)
+{
+    AttendLayout l;
+    l.prefix = align256(kSlotBytes);
+    l.part_o = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 1));
+    l.part_ml = l.part_o + (size_t)2 * kMaxGrid * 16 * (size_t)D * sizeof(float);
+    l.lse2 = l.part_ml + (size_t)2 * kMaxGrid * 16 * sizeof(float2);
+    l.bytes = l.lse2 + (weights ? align256(sizeof(float) * (size_t)(B * Hq * Sq)) : 0);
+    return l;
+}
+
+template <int D>
+cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st)
+{
+    const size_t smem = sizeof(AttendSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 1);
+    cudaError_t e = cudaFuncSetAttribute(kv8_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = 2 * num_sms() < kMaxGrid ? 2 * num_sms() : kMaxGrid;
+    kv8_attend_kernel<D><<<grid, kThreadsA, smem, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int rts = (a.Sq * a.G + 15) / 16;
+    kv8_join_kernel<D><<<(unsigned)(a.B * a.c.heads * rts), 128, 0, st>>>(a, rts, grid);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (a.w) {
+        const int64_t most = a.slots < a.L ? a.slots : a.L;
+        const dim3 wg((unsigned)((most + 16 * kWarps - 1) / (16 * kWarps)), (unsigned)a.c.heads, (unsigned)a.B);
+        kv8_weights_kernel<D><<<wg, kThreadsA, 0, st>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace
+}  // namespace hq
+
+using namespace hq;
+
+extern "C" size_t hq_kv8_attend_workspace_bytes(int64_t B, int64_t Hq, int64_t Sq, int32_t D, int32_t weights)
+{
+    if (B < 1 || B > kMaxBatch || Hq < 1 || Sq < 1 || (D != 64 && D != 128) || Hq > 65535 || Sq > ((int64_t)1 << 24)) return 0;
+    return attend_layout(B, Hq, Sq, D, weights != 0).bytes;
+}
+
+extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!p || !kv8_cache_ok(&p->cache) || !p->q || !p->out || !p->table || !p->lens || !ws) return HQ_ERR_ARG;
+    if (!kv8_shape_supported(&p->cache)) return HQ_ERR_UNSUPPORTED;
+    const int64_t H = p->cache.heads, page = p->cache.page;
+    if (p->B < 1 || p->Sq < 1 || p->Hq < H || p->Hq % H || p->max_pages < 1 || p->table_stride < p->max_pages) return HQ_ERR_ARG;
+    if (!(p->scale == p->scale) || p->scale - p->scale != 0.0f) return HQ_ERR_ARG;
+    if (p->B > kMaxBatch || p->Hq > 65535 || p->Sq > ((int64_t)1 << 24) || p->max_pages > ((int64_t)1 << 24)) return HQ_ERR_UNSUPPORTED;
+    const int64_t G = p->Hq / H, rts = (p->Sq * G + 15) / 16, slots = p->max_pages * page;
+    // share units and thread blocks are counted in 31 bits, slots of a sequence too
+    if (slots > ((int64_t)1 << 30) || p->Sq * G > ((int64_t)1 << 26) || p->B * H > ((int64_t)1 << 26) ||
+        p->B * H * rts > ((int64_t)1 << 31) / ((slots + kTile - 1) / kTile))
+        return HQ_ERR_UNSUPPORTED;
+    const int64_t qs = p->q_stride[0] | p->q_stride[1] | p->q_stride[2];
+    const int64_t os = p->out_stride[0] | p->out_stride[1] | p->out_stride[2];
+    if ((qs | os) & 7) return HQ_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(p->q) | reinterpret_cast<uintptr_t>(p->out)) & 15u) return HQ_ERR_ARG;
+    const uintptr_t al = reinterpret_cast<uintptr_t>(p->table) | reinterpret_cast<uintptr_t>(p->lens) |
+                         reinterpret_cast<uintptr_t>(p->q_lens) | reinterpret_cast<uintptr_t>(p->lse) |
+                         reinterpret_cast<uintptr_t>(p->weights) | reinterpret_cast<uintptr_t>(p->weights_in);
+    if ((al & 3u) || (reinterpret_cast<uintptr_t>(ws) & 255u)) return HQ_ERR_ARG;
+    if (p->weights && p->L < 1) return HQ_ERR_ARG;
+    if (p->weights_in && !p->weights) return HQ_ERR_ARG;
+    if (p->weights && p->B > 65535) return HQ_ERR_UNSUPPORTED;
+    const AttendLayout l = attend_layout(p->B, p->Hq, p->Sq, p->cache.dim, p->weights != nullptr);
+    if (ws_bytes < l.bytes) return HQ_ERR_ARG;
+    DeviceGuard dev(p->cache.k);
+    if (!dev.ok) return HQ_ERR_ARG;
+    AttendArgs a;
+    a.c = p->cache;
+    a.q = static_cast<const __nv_bfloat16*>(p->q);
+    a.qb = p->q_stride[0];
+    a.qh = p->q_stride[1];
+    a.qs = p->q_stride[2];
+    a.out = static_cast<__nv_bfloat16*>(p->out);
+    a.ob = p->out_stride[0];
+    a.oh = p->out_stride[1];
+    a.os = p->out_stride[2];
+    a.B = (int)p->B;
+    a.Hq = (int)p->Hq;
+    a.Sq = (int)p->Sq;
+    a.G = (int)G;
+    a.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
+    a.table = p->table;
+    a.table_stride = p->table_stride;
+    a.slots = slots;
+    a.lens = p->lens;
+    a.q_lens = p->q_lens;
+    a.scale = p->scale;
+    a.causal = p->causal;
+    a.lse = p->lse;
+    a.lb = p->lse_stride[0];
+    a.lh = p->lse_stride[1];
+    a.win = p->weights_in;
+    a.w = p->weights;
+    a.wib = p->win_stride[0];
+    a.wih = p->win_stride[1];
+    a.wb = p->w_stride[0];
+    a.wh = p->w_stride[1];
+    a.L = p->L;
+    char* base = static_cast<char*>(ws);
+    a.prefix = reinterpret_cast<uint32_t*>(base + l.prefix);
+    a.part_o = reinterpret_cast<float*>(base + l.part_o);
+    a.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
+    a.lse2 = p->weights ? reinterpret_cast<float*>(base + l.lse2) : nullptr;
+    a.ws = static_cast<WsHeader*>(ws);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = p->cache.dim == 64 ? launch_attend<64>(a, st) : launch_attend<128>(a, st);
+    return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+}

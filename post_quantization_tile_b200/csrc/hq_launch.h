@@ -52,6 +52,26 @@ cudaError_t launch_merge_nonfinite(void* ws, const uint32_t* nonfinite, cudaStre
 bool tensor_map_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int es, int box_rows);
 // make the device that owns p current (hq_api.cu)
 bool device_of(const void* p);
+// the device that owns p, made current while this lives (the caller's device is put back)
+struct DeviceGuard {
+    explicit DeviceGuard(const void* p)
+    {
+        if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+        ok = device_of(p);
+    }
+    ~DeviceGuard()
+    {
+        int cur = -1;
+        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+    }
+    DeviceGuard(const DeviceGuard&) = delete;
+    DeviceGuard& operator=(const DeviceGuard&) = delete;
+    int prev = -1;
+    bool ok = false;
+};
+// 2-D tensor map of a row-major byte matrix [rows, cols] with a row pitch of ld bytes (a multiple of
+// 16): box [box_rows][128 bytes], 128-byte swizzle, zeros outside (hq_api.cu)
+bool tensor_map_bytes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 // workspace bytes of the encoder for one source (0 bf16, 1 fp32 weights, 2 coefficients); 0 if
 // the shape is invalid (hq_api.cu)
 size_t encode_workspace_bytes(int64_t rows, int64_t cols, int32_t n, int src);
