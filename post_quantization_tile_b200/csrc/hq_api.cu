@@ -477,6 +477,19 @@ bool tensor_map_bytes(CUtensorMap* m, const void* base, int64_t rows, int64_t co
 {
     return make_map(m, base, rows, cols, 1, box_rows, ld);
 }
+
+bool tensor_map_kv8(CUtensorMap* m, const void* base, int64_t rows, int dim, int box_rows)
+{
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)dim, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)dim};
+    const cuuint32_t box[2] = {(cuuint32_t)dim, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 size_t encode_workspace_bytes(int64_t rows, int64_t cols, int32_t n, int src)
 {
     return valid_tile(n) ? ws_bytes_for_src(rows, cols, n, src) : 0;

@@ -10,14 +10,17 @@
 // accumulator in the workspace and a second small kernel joins them.
 //
 // Codes become binary16 in registers (one conversion instruction for two codes, exact) and both
-// products run on the matrix instruction m16n8k16 with binary32 accumulators.  The order of the
-// contraction and of the output columns is free, so every lane loads 16 contiguous bytes of a key or
-// value row straight from global memory into the places its fragments need: no shared memory and
-// no transposition but byte pairs of two value rows.
+// products run on the matrix instruction m16n8k16 with binary32 accumulators.  Sixteen tokens of one
+// head are contiguous (a page holds a multiple of sixteen), so every warp streams its groups of
+// sixteen keys and values with two TMA boxes each into a ring of its own, without any barrier between
+// warps.  The order of the contraction and of the output columns is free: every lane reads 16
+// contiguous bytes of a key or value row as the fragments it needs, the boxes' swizzle keeps those
+// reads free of bank conflicts, and nothing is transposed but byte pairs of two value rows.
 //   - queries become binary16 after a power-of-two scaling per row (bf16's 8 bits fit exactly, elements
 //     below 2^-38 of the row's largest lose bits);
-//   - probabilities become binary16 at 2^10 times their value relative to the running maximum: 11
-//     bits, and weights down to 2^-34 of the largest still count;
+//   - probabilities become binary16 at 2^7 times their value relative to a running reference, which
+//     moves up to the maximum when that is more than 2^8 larger: 11 bits, at most 2^15, and weights
+//     down to 2^-31 of the largest still count;
 //   - key scales multiply the scores, value scales stay out of the products: the accumulator is kept in
 //     units of the last value scale and multiplied by the (power-of-two) ratio when that changes.
 #include <cuda_runtime.h>
@@ -31,7 +34,9 @@ constexpr int kWarps = 4, kThreadsA = 32 * kWarps;
 constexpr int kTile = 64;         // tokens of one share unit
 constexpr int kMaxBatch = 4096;   // sequences of one call (their prefix sums live in shared memory)
 constexpr int kMaxGrid = 512;
-constexpr float kBoost = 10.0f;   // probabilities are held times 2^10
+constexpr int kStages = 4;        // ring of sixteen-token groups per warp
+constexpr float kBoost = 7.0f;    // probabilities are held times 2^7, and up to 2^8 times that
+constexpr float kSlack = 8.0f;    // before a larger maximum moves the reference they are relative to
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttendArgs {
@@ -122,7 +127,7 @@ struct QueryRows {
             uint32_t m = 0;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                w[kk] = is ? __ldg(reinterpret_cast<const uint2*>(q + (kk >> 2) * 64 + t * 16 + (kk & 3) * 4)) : make_uint2(0u, 0u);
+                w[kk] = is ? __ldg(reinterpret_cast<const uint2*>(q + t * (D / 4) + kk * 4)) : make_uint2(0u, 0u);
                 m = max(m, max(max((w[kk].x << 16) & 0x7FFF0000u, w[kk].x & 0x7FFF0000u),
                                max((w[kk].y << 16) & 0x7FFF0000u, w[kk].y & 0x7FFF0000u)));
             }
@@ -141,20 +146,36 @@ struct QueryRows {
     }
 };
 
-// sixteen tokens' keys: lane (g, t) holds 16-byte runs of the two tokens whose scores are the columns g
-// of its two score tiles
+// byte offset of 16-byte chunk c of row r in a swizzled TMA box of D-byte rows
+template <int D>
+__device__ __forceinline__ uint32_t swz_row(int r, int c)
+{
+    return (uint32_t)(r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+}
+
+// sixteen tokens' keys: lane (g, t) holds dims t D/4 .. of tokens g and g + 8, whose scores are the
+// columns g of its two score tiles
 template <int D>
 struct KeyGroup {
     uint4 w[2][D / 64];
 
-    __device__ __forceinline__ void load(const uint8_t* k, bool ok)
+    __device__ __forceinline__ void load(const unsigned char* box)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < D / 64; ++j)
-                w[i][j] = ok ? __ldg(reinterpret_cast<const uint4*>(k + (4 * (g >> 1) + (g & 1) + 2 * i) * D + j * 64 + t * 16))
+                w[i][j] = *reinterpret_cast<const uint4*>(box + swz_row<D>(g + 8 * i, t * (D / 64) + j));
+    }
+    __device__ __forceinline__ void load_global(const uint8_t* k, bool ok)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+                w[i][j] = ok ? __ldg(reinterpret_cast<const uint4*>(k + (g + 8 * i) * D + t * (D / 4) + j * 16))
                              : make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ void scores(const QueryRows<D>& q, float (&s)[2][4]) const
@@ -173,29 +194,31 @@ struct KeyGroup {
     }
 };
 
-// sixteen tokens' values: lane (g, t) holds dims g D/8 .. of tokens 4 t .. 4 t + 3
+// sixteen tokens' values: lane (g, t) holds dims g D/8 .. of tokens 2 t, 2 t + 1, 2 t + 8 and 2 t + 9
 template <int D>
 struct ValueGroup {
     uint32_t w[4][D / 32];
 
-    __device__ __forceinline__ void load(const uint8_t* v, bool ok, int left)
+    __device__ __forceinline__ void load(const unsigned char* box, int left)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint8_t* at = v + (4 * t + i) * D + g * (D / 8);
-            const bool is = ok && 4 * t + i < left;  // slots nobody sees may hold anything: zero times NaN
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) w[i][j] = 0u;
-            if (is) {
-                if (D == 128) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
-                    w[i][0] = x.x, w[i][1] = x.y, w[i][D / 32 - 2] = x.z, w[i][D / 32 - 1] = x.w;
-                } else {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
-                    w[i][0] = x.x, w[i][1] = x.y;
-                }
+            const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+            if (D == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(box + swz_row<D>(r, g));
+                w[i][0] = x.x, w[i][1] = x.y, w[i][D / 32 - 2] = x.z, w[i][D / 32 - 1] = x.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(box + swz_row<D>(r, g >> 1) + (g & 1) * 8);
+                w[i][0] = x.x, w[i][1] = x.y;
             }
+        }
+        if (left < 16) {  // slots nobody sees may hold anything: zero times NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (2 * t + (i & 1) + 8 * (i >> 1) >= left)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) w[i][j] = 0u;
         }
     }
     __device__ __forceinline__ void accumulate(const uint32_t (&p)[4], float (&o)[D / 8][4]) const
@@ -212,20 +235,21 @@ struct ValueGroup {
     }
 };
 
-// where sixteen tokens from slot `tok` lie; false if their page is outside the pool
-__device__ __forceinline__ bool locate(const AttendArgs& a, const int32_t* table, int h, int tok, int64_t& ph, int64_t& row)
+// first cache row (of [page][head][token]) of sixteen tokens from slot `tok`; -1 if their page is
+// outside the pool.  The entry points keep the number of rows below 2^31.
+__device__ __forceinline__ int locate(const AttendArgs& a, const int32_t* table, int h, int tok)
 {
     const int32_t id = __ldg(table + (tok >> a.page_shift));
-    const bool ok = id >= 0 && id < a.c.pages;
-    ph = ok ? (int64_t)id * a.c.heads + h : 0;
-    row = (ph << a.page_shift) + (tok & (a.c.page - 1));
-    return ok;
+    return id >= 0 && id < a.c.pages ? (int)(((uint32_t)id * a.c.heads + h) << a.page_shift) + (tok & (a.c.page - 1)) : -1;
 }
 
 template <int D>
 struct AttendSmem {
+    unsigned char ring[kWarps][kStages][2][16 * D];  // keys, values of a group (TMA boxes: 1024-byte aligned)
     float o[kWarps][16][D + 4];
     float m[kWarps][16], l[kWarps][16];
+    float2 scale[kWarps][kStages];  // of the group's keys and values; values < 0: no such page
+    uint64_t full[kWarps][kStages];
     uint32_t scan[kWarps];
     uint32_t status;
 };
@@ -246,13 +270,19 @@ __device__ __forceinline__ void write_lse(const AttendArgs& a, int b, int h, int
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreadsA, 2) kv8_attend_kernel(const AttendArgs a)
+__global__ void __launch_bounds__(kThreadsA, 2)
+    kv8_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv)
 {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    AttendSmem<D>& sm = *reinterpret_cast<AttendSmem<D>*>(smem_raw);
-    uint32_t* pre = reinterpret_cast<uint32_t*>(smem_raw + sizeof(AttendSmem<D>));
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    AttendSmem<D>& sm = *reinterpret_cast<AttendSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint32_t* pre = reinterpret_cast<uint32_t*>(&sm + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    if (tid == 0) sm.status = 0u;
+    if (tid == 0) {
+        sm.status = 0u;
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[w][i], 1);
+        fence_mbar_init();
+    }
     // prefix sums of the sequences' share units
     {
         const int run = (a.B + kThreadsA - 1) / kThreadsA, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
@@ -288,7 +318,9 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_attend_kernel(const AttendAr
     const uint32_t shares = min(W, gridDim.x);  // none is empty: the join walks a unit's shares one by one
     uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
     const uint32_t w1 = blockIdx.x < shares ? (uint32_t)((uint64_t)(blockIdx.x + 1) * W / shares) : 0u;
-    bool bad = false;
+    uint32_t status = 0u;
+    bool dead = false;  // after a timeout a warp only walks the loops, so that all reach the barriers
+    uint32_t it = 0;  // groups this warp has issued before this unit: ring stage and parity
     while (w0 < w1) {
         // the unit that share unit w0 belongs to
         int b = 0;
@@ -315,39 +347,80 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_attend_kernel(const AttendAr
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vref = 1.0f;
 
-        for (int gr = (int)t0 * (kTile / 16) + warp; gr < groups; gr += kWarps) {
-            const int tok = gr * 16;
-            int64_t ph, row;
-            const bool ok = locate(a, table, h, tok, ph, row);
-            bad |= !ok;
+        // this warp's groups: every kWarps-th; their page rows and scales are fetched 32 at a time, one
+        // per lane, and the boxes of kStages groups are under way at any time
+        const int gr0 = (int)t0 * (kTile / 16) + warp, count = gr0 < groups && !dead ? (groups - gr0 + kWarps - 1) / kWarps : 0;
+        int my_row = -1;
+        float2 my_scale = make_float2(0.0f, -1.0f);
+        auto issue = [&](int i) {
+            if ((i & 31) == 0) {
+                my_row = i + lane < count ? locate(a, table, h, (gr0 + (i + lane) * kWarps) * 16) : -1;
+                if (my_row >= 0) {
+                    const int ph = my_row >> a.page_shift;
+                    my_scale = make_float2(__ldg(a.c.k_scale + ph), __ldg(a.c.v_scale + ph));
+                } else {
+                    my_scale.y = -1.0f;
+                    if (i + lane < count) status |= kStRange;
+                }
+            }
+            const int row = __shfl_sync(0xFFFFFFFFu, my_row, i & 31);
+            const float ks = __shfl_sync(0xFFFFFFFFu, my_scale.x, i & 31), vs = __shfl_sync(0xFFFFFFFFu, my_scale.y, i & 31);
+            if (lane == 0) {
+                const uint32_t st = (it + i) % kStages;
+                sm.scale[warp][st] = make_float2(ks, vs);
+                if (row >= 0) {
+                    mbar_arrive_expect_tx(&sm.full[warp][st], 32 * D);
+                    tma_load_2d(sm.ring[warp][st][0], &tk, 0, row, &sm.full[warp][st]);
+                    tma_load_2d(sm.ring[warp][st][1], &tv, 0, row, &sm.full[warp][st]);
+                } else {
+                    mbar_arrive(&sm.full[warp][st]);
+                }
+            }
+        };
+        for (int i = 0; i < kStages && i < count; ++i) issue(i);
+        __syncwarp();
+        for (int i = 0; i < count; ++i) {
+            const uint32_t st = (it + i) % kStages;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][st], ((it + i) / kStages) & 1))) {
+                status |= kStTimeout;  // the copies of the other stages are waited for below
+                for (int j = i + 1; j < count && j < i + kStages; ++j)
+                    mbar_wait(&sm.full[warp][(it + j) % kStages], ((it + j) / kStages) & 1);
+                dead = true;
+                break;
+            }
+            const int tok = (gr0 + i * kWarps) * 16;
+            const float ks = sm.scale[warp][st].x, vs = sm.scale[warp][st].y;
             KeyGroup<D> k;
             ValueGroup<D> v;
-            k.load(a.c.k + row * D, ok);
-            v.load(a.c.v + row * D, ok, end - tok);
-            const float ks = __ldg(a.c.k_scale + ph), vs = ok ? __ldg(a.c.v_scale + ph) : vref;
+            k.load(sm.ring[warp][st][0]);
+            v.load(sm.ring[warp][st][1], end - tok);
+            __syncwarp();  // the stage is in registers: fill it again
+            if (i + kStages < count) issue(i + kStages);
+            if (vs < 0.0f) continue;
             float x[2][4];
             k.scores(q, x);
             float top[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const float c = q.c[half] * ks;
-                const int left = ok ? q.end[half] - tok : 0;
+                const int left = q.end[half] - tok;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        x[i][2 * half + e] = 4 * t + 2 * i + e < left ? x[i][2 * half + e] * c : -INFINITY;
+                        x[i][2 * half + e] = 2 * t + 8 * i + e < left ? x[i][2 * half + e] * c : -INFINITY;
                 top[half] = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
                 top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
                 top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 2));
-                top[half] = fmaxf(top[half], m[half]);
             }
-            // a changed maximum or value scale changes the accumulator's units
-            const float vr = vref / vs;
-            if (__any_sync(0xFFFFFFFFu, top[0] != m[0] || top[1] != m[1] || vr != 1.0f)) {
+            // a reference that moves or another value scale changes the accumulator's units
+            const bool moves = top[0] > m[0] + kSlack || top[1] > m[1] + kSlack || vs != vref;
+            if (__any_sync(0xFFFFFFFFu, moves)) {
+                const float vr = __fdiv_rn(vref, vs);
                 float f[2];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
+                    top[half] = top[half] > m[half] + kSlack ? top[half] : m[half];
                     f[half] = m[half] == -INFINITY ? 1.0f : ex2(m[half] - top[half]);
                     l[half] *= f[half];
                     f[half] *= vr;
@@ -377,6 +450,8 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_attend_kernel(const AttendAr
                                    pack_f16(x[1][2], x[1][3])};
             v.accumulate(p, o);
         }
+
+        it += count;
 
         // join the warps: their accumulators through shared memory, each at the common maximum
 #pragma unroll
@@ -438,7 +513,7 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_attend_kernel(const AttendAr
         __syncthreads();
         w0 += t1 - t0;
     }
-    if (bad) atomicOr(&sm.status, kStRange);
+    if (status) atomicOr(&sm.status, status);
     __syncthreads();
     if (tid == 0) slot_write(a.ws, gridDim.x, blockIdx.x, sm.status, 0u);
 }
@@ -466,7 +541,9 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const AttendArgs a, int r
 #pragma unroll
     for (int d = 0; d < DPT; ++d) y[d] = 0.0f;
     if (tiles) {
+#pragma unroll 4
         for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * c + (c == c0)) * 16 + r].x);
+#pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
             const int64_t at = (int64_t)(2 * c + (c == c0)) * 16 + r;
             const float2 ml = a.part_ml[at];
@@ -500,11 +577,11 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
     const int n = (int)min((int64_t)s.n, a.L);
     const int tok = (blockIdx.x * kWarps + warp) * 16;
     if (tok >= n) return;
-    int64_t ph, row;
-    const bool ok = locate(a, a.table + b * a.table_stride, h, tok, ph, row);
+    const int row = locate(a, a.table + b * a.table_stride, h, tok);
+    const bool ok = row >= 0;
     KeyGroup<D> k;
-    k.load(a.c.k + row * D, ok);
-    const float ks = __ldg(a.c.k_scale + ph);
+    k.load_global(a.c.k + (int64_t)(ok ? row : 0) * D, ok);
+    const float ks = ok ? __ldg(a.c.k_scale + (row >> a.page_shift)) : 0.0f;
     float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
     const float* lse2 = a.lse2 + ((int64_t)b * a.c.heads + h) * a.G * a.Sq;
     const int rts = row_tiles(a, s.m);
@@ -522,7 +599,7 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (4 * t + 2 * i + e < left) sum[i][e] += ex2(x[i][2 * half + e] * c - l2);
+                    if (2 * t + 8 * i + e < left) sum[i][e] += ex2(x[i][2 * half + e] * c - l2);
         }
     }
     const float* win = a.win ? a.win + b * a.wib + h * a.wih : nullptr;
@@ -534,7 +611,7 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
             float x = sum[i][e];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-            const int j = tok + 4 * t + 2 * i + e;
+            const int j = tok + 2 * t + 8 * i + e;
             if (g == 0 && j < n) w[j] = win ? win[j] + x : x;
         }
 }
@@ -558,11 +635,14 @@ AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool we
 template <int D>
 cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st)
 {
-    const size_t smem = sizeof(AttendSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 1);
+    CUtensorMap tk, tv;
+    const int64_t rows = a.c.pages * a.c.heads * a.c.page;
+    if (!tensor_map_kv8(&tk, a.c.k, rows, D, 16) || !tensor_map_kv8(&tv, a.c.v, rows, D, 16)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + sizeof(AttendSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 1);
     cudaError_t e = cudaFuncSetAttribute(kv8_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int grid = 2 * num_sms() < kMaxGrid ? 2 * num_sms() : kMaxGrid;
-    kv8_attend_kernel<D><<<grid, kThreadsA, smem, st>>>(a);
+    kv8_attend_kernel<D><<<grid, kThreadsA, smem, st>>>(a, tk, tv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rts = (a.Sq * a.G + 15) / 16;
     kv8_join_kernel<D><<<(unsigned)(a.B * a.c.heads * rts), 128, 0, st>>>(a, rts, grid);
@@ -596,6 +676,7 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     if (!(p->scale == p->scale) || p->scale - p->scale != 0.0f) return HQ_ERR_ARG;
     if (p->B > kMaxBatch || p->Hq > 65535 || p->Sq > ((int64_t)1 << 24) || p->max_pages > ((int64_t)1 << 24)) return HQ_ERR_UNSUPPORTED;
     const int64_t G = p->Hq / H, rts = (p->Sq * G + 15) / 16, slots = p->max_pages * page;
+    if (p->cache.pages * H > (((int64_t)1 << 31) - 1) / page) return HQ_ERR_UNSUPPORTED;  // cache rows in 31 bits
     // share units and thread blocks are counted in 31 bits, slots of a sequence too
     if (slots > ((int64_t)1 << 30) || p->Sq * G > ((int64_t)1 << 26) || p->B * H > ((int64_t)1 << 26) ||
         p->B * H * rts > ((int64_t)1 << 31) / ((slots + kTile - 1) / kTile))

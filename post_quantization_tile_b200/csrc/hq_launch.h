@@ -72,6 +72,8 @@ struct DeviceGuard {
 // 2-D tensor map of a row-major byte matrix [rows, cols] with a row pitch of ld bytes (a multiple of
 // 16): box [box_rows][128 bytes], 128-byte swizzle, zeros outside (hq_api.cu)
 bool tensor_map_bytes(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
+// 2-D tensor map of [rows, dim] bytes (dim 64 or 128): box [box_rows][dim], swizzle of dim bytes (hq_api.cu)
+bool tensor_map_kv8(CUtensorMap* m, const void* base, int64_t rows, int dim, int box_rows);
 // workspace bytes of the encoder for one source (0 bf16, 1 fp32 weights, 2 coefficients); 0 if
 // the shape is invalid (hq_api.cu)
 size_t encode_workspace_bytes(int64_t rows, int64_t cols, int32_t n, int src);
