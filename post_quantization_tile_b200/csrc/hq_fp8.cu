@@ -16,8 +16,15 @@
 namespace hq {
 namespace {
 
-constexpr int kQThreads = 256;
-constexpr int kQRows = kQThreads / 16;  // rows of one pass of the thread block
+// threads of a block and row passes over its tile: 32 rows x 128 columns for blocks of 1 x 128, the
+// 128 x 128 block itself otherwise
+template <int BLOCK>
+struct QuantCfg {
+    static constexpr int THREADS = BLOCK == 128 ? 512 : 256;
+    static constexpr int ROWS = THREADS / 16;  // rows of one pass
+    static constexpr int PASSES = BLOCK == 128 ? 4 : 2;
+    static constexpr int TILE = ROWS * PASSES;
+};
 
 struct QuantArgs {
     const void* x;
@@ -28,13 +35,13 @@ struct QuantArgs {
     WsHeader* ws;
 };
 
-// PASSES row passes per tile of 16 * PASSES rows by 128 columns; BLOCK: rows of a scale block (1 or
-// the whole tile of 128); VEC: rows of x start on 16 bytes
+// BLOCK: rows of a scale block (1 or the whole tile of 128); VEC: rows of x start on 16 bytes
 template <typename T, int BLOCK, bool VEC>
-__global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs a)
+__global__ void __launch_bounds__(QuantCfg<BLOCK>::THREADS, sizeof(T) == 2 ? 2048 / QuantCfg<BLOCK>::THREADS - 1 : 1024 / QuantCfg<BLOCK>::THREADS)
+    fp8_quantize_kernel(const QuantArgs a)
 {
-    constexpr int PASSES = BLOCK == 128 ? 8 : 2;
-    constexpr int TILE = PASSES * kQRows;
+    constexpr int kQThreads = QuantCfg<BLOCK>::THREADS, kQRows = QuantCfg<BLOCK>::ROWS;
+    constexpr int PASSES = QuantCfg<BLOCK>::PASSES, TILE = QuantCfg<BLOCK>::TILE;
     __shared__ uint32_t warp_max[kQThreads / 32];
     __shared__ uint32_t s_status, s_nonfinite;
     const int sub = threadIdx.x & 15, row16 = threadIdx.x >> 4;
@@ -45,25 +52,20 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
         const int64_t r0 = (tile % a.tiles_r) * TILE;
         const int64_t kb = tile / a.tiles_r;
         const int64_t c = kb * 128 + sub * 8;  // this lane's first column
-        float v[PASSES][8];
+        Raw8<T> v[PASSES];
         uint32_t m[PASSES];
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
             const int64_t r = r0 + p * kQRows + row16;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+            v[p].zero();
             if (r < a.rows) {
                 const T* at = x + r * a.ldx + c;
-                if (VEC && c + 8 <= a.cols) {
-                    load8(at, v[p]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c + i < a.cols) v[p][i] = load1(at + i);
-                }
+                if (VEC && c + 8 <= a.cols) v[p].load(at);
+                else v[p].load_part(at, a.cols - c);
             }
-            m[p] = amax_bits8(v[p]);
         }
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) m[p] = v[p].amax_bits();
         if (BLOCK == 1) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p)
@@ -113,8 +115,8 @@ cudaError_t launch_quantize(const QuantArgs& a, bool vec, cudaStream_t st)
 {
     const int64_t most = kMaxSlots;
     const int grid = (int)(a.tiles < most ? a.tiles : most);
-    if (vec) fp8_quantize_kernel<T, BLOCK, true><<<grid, kQThreads, 0, st>>>(a);
-    else fp8_quantize_kernel<T, BLOCK, false><<<grid, kQThreads, 0, st>>>(a);
+    if (vec) fp8_quantize_kernel<T, BLOCK, true><<<grid, QuantCfg<BLOCK>::THREADS, 0, st>>>(a);
+    else fp8_quantize_kernel<T, BLOCK, false><<<grid, QuantCfg<BLOCK>::THREADS, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -149,7 +151,7 @@ extern "C" hq_status_t hq_fp8_quantize(const void* x, hq_dtype_t dtype, int64_t 
     a.ldq = ldq;
     a.q = q;
     a.scale = scale;
-    a.tiles_r = block == 128 ? (rows + 127) / 128 : (rows + 2 * kQRows - 1) / (2 * kQRows);
+    a.tiles_r = block == 128 ? (rows + 127) / 128 : (rows + QuantCfg<1>::TILE - 1) / QuantCfg<1>::TILE;
     a.tiles = a.tiles_r * ((cols + 127) / 128);
     a.ws = static_cast<WsHeader*>(ws);
     const bool vec = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)ldx * es) & 15u) == 0;

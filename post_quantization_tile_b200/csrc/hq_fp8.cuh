@@ -80,37 +80,77 @@ __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((127 + 
 // the largest magnitude the largest scale can hold (448 * 2^40), as a bit pattern
 constexpr uint32_t kAmaxLimit = ((127u + 48u) << 23) | 0x600000u;
 
-// eight elements from 16-byte aligned memory as binary32
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8])
-{
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    v[0] = bf16lo_to_f32(w.x), v[1] = bf16hi_to_f32(w.x), v[2] = bf16lo_to_f32(w.y), v[3] = bf16hi_to_f32(w.y);
-    v[4] = bf16lo_to_f32(w.z), v[5] = bf16hi_to_f32(w.z), v[6] = bf16lo_to_f32(w.w), v[7] = bf16hi_to_f32(w.w);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8])
-{
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
+// eight elements of a row as they lie in memory (bf16: four words, fp32: eight), kept so between their
+// maximum and their codes
+template <typename T>
+struct Raw8;
 
-// largest bit pattern of |v|: above 0x7F7FFFFF where an element is infinite or NaN
-__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8])
-{
-    uint32_t m = 0;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p)  // 16-byte aligned
+    {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    }
+    __device__ __forceinline__ void load_part(const __nv_bfloat16* p, int64_t left)  // any alignment, `left` elements
+    {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return m;
-}
+        for (int i = 0; i < 8; ++i)
+            if (i < left) w[i >> 1] |= (uint32_t)__bfloat16_as_ushort(p[i]) << (16 * (i & 1));
+    }
+    // bit pattern (binary32) of the largest magnitude: above kFiniteMax where an element is infinite or NaN
+    __device__ __forceinline__ uint32_t amax_bits() const
+    {
+        __nv_bfloat162 m = __habs2(at(0));
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(at(i)));
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(&m) & 0x7FFF7FFFu;
+        return max(b & 0xFFFF0000u, b << 16);
+    }
+    __device__ __forceinline__ float2 get(int i) const { return make_float2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i])); }
+    __device__ __forceinline__ __nv_bfloat162 at(int i) const { return *reinterpret_cast<const __nv_bfloat162*>(&w[i]); }
+};
+
+template <>
+struct Raw8<float> {
+    float v[8];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+    __device__ __forceinline__ void load(const float* p)
+    {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    __device__ __forceinline__ void load_part(const float* p, int64_t left)
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) v[i] = p[i];
+    }
+    __device__ __forceinline__ uint32_t amax_bits() const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        return m;
+    }
+    __device__ __forceinline__ float2 get(int i) const { return make_float2(v[2 * i], v[2 * i + 1]); }
+};
+
 constexpr uint32_t kFiniteMax = 0x7F7FFFFFu;
 
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv)
+// the codes of eight elements, inv = 1 / scale
+template <typename T>
+__device__ __forceinline__ uint2 encode8(const Raw8<T>& x, float inv)
 {
-    uint2 w;
-    w.x = e4m3x4(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv), __fmul_rn(v[2], inv), __fmul_rn(v[3], inv));
-    w.y = e4m3x4(__fmul_rn(v[4], inv), __fmul_rn(v[5], inv), __fmul_rn(v[6], inv), __fmul_rn(v[7], inv));
-    return w;
+    const float2 i2 = make_float2(inv, inv);
+    const float2 a = f2mul(x.get(0), i2), b = f2mul(x.get(1), i2), c = f2mul(x.get(2), i2), d = f2mul(x.get(3), i2);
+    return make_uint2(e4m3x4(a.x, a.y, b.x, b.y), e4m3x4(c.x, c.y, d.x, d.y));
 }
 
 }  // namespace hq

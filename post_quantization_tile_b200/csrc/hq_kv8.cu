@@ -26,27 +26,26 @@ struct AppendArgs {
     int64_t table_stride, max_pages;
     const int32_t* lens;
     const int32_t* n_new;
-    int64_t span, units;  // pages a sequence's new tokens can touch; 2 * B * heads * span
+    uint32_t span, units;  // pages a sequence's new tokens can touch; 2 * B * heads * span
     WsHeader* ws;
 };
 
-template <typename T, int D>
+// PASSES: row passes over a page
+template <typename T, int D, int PASSES>
 __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs a)
 {
     constexpr int LPR = D / 8;                // lanes of one row
     constexpr int RPP = kAThreads / LPR;      // rows of one pass
-    constexpr int PASSES = 128 / RPP;         // passes of the largest page
     __shared__ uint32_t warp_max[kAThreads / 32];
     __shared__ uint32_t s_status, s_nonfinite;
     const int sub = threadIdx.x % LPR, row = threadIdx.x / LPR;
     if (threadIdx.x == 0) s_status = 0u, s_nonfinite = 0u;
     __syncthreads();
     const int page = a.c.page;
-    for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
-        const int64_t sp = u % a.span;
-        const int kv = (int)(u / a.span % 2);
-        const int h = (int)(u / (2 * a.span) % a.c.heads);
-        const int64_t b = u / (2 * a.span * a.c.heads);
+    for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x) {
+        const uint32_t rest = u / a.span, sp = u - rest * a.span;
+        const int kv = rest & 1;
+        const int b = (int)((rest >> 1) / (uint32_t)a.c.heads), h = (int)((rest >> 1) - (uint32_t)b * a.c.heads);
         int64_t first = a.lens[b];
         int64_t n = a.n_new ? (int64_t)a.n_new[b] : a.S;
         const bool odd = first < 0 || n < 0 || n > a.S || first + n > a.max_pages * page;
@@ -67,20 +66,21 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
         uint8_t* codes = (kv ? a.c.v : a.c.k) + ph * page * D;
         float* scale = (kv ? a.c.v_scale : a.c.k_scale) + ph;
         const float s_old = lo > 0 ? *scale : 0.0f;
-        float v[PASSES][8];
+        Raw8<T> v[PASSES];
         uint32_t top = 0;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
             const int r = p * RPP + row;
+            v[p].zero();
+            if (r >= lo && r < hi) v[p].load(x + r * a.ss[kv] + sub * 8);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-            if (r >= lo && r < hi) load8(x + r * a.ss[kv] + sub * 8, v[p]);
-            uint32_t m = amax_bits8(v[p]);
+        for (int p = 0; p < PASSES; ++p) {
+            uint32_t m = v[p].amax_bits();
 #pragma unroll
             for (int o = LPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             if (m > kFiniteMax) {  // a token with NaN or infinity is kept as zeros
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+                v[p].zero();
                 if (sub == 0) atomicOr(&s_status, kStNonfinite), atomicAdd(&s_nonfinite, 1u);
                 m = 0;
             }
@@ -116,12 +116,15 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
 
 // ------------------------------------------------------------------------------------------------
 // Evict, first step: which slots of a (sequence, head) stay.  The last `recent` do; of the others the
-// budget - recent with the largest weights, the lower slot first among equals.  The weight that
-// divides them is found digit by digit (four histograms of 8 bits over order-preserving keys), then
-// every thread takes a run of consecutive slots, counts, and writes its kept ones behind those of the
-// threads before it, so the kept slots come out in order.
+// budget - recent with the largest weights, the lower slot first among equals.  One thread block reads
+// the weights once, as order-preserving keys in shared memory (as many as fit; the rest are read
+// again), and finds the key that divides them digit by digit: histograms of 11, 11 and 10 bits, each
+// with a scan from the largest digit down.  Then every thread takes a run of consecutive slots, counts,
+// and writes its kept ones behind those of the threads before it, so the kept slots come out in order.
 // ------------------------------------------------------------------------------------------------
 constexpr int kEThreads = 1024;
+constexpr int kEBins = 2048;
+constexpr int64_t kEKeys = 40 * 1024;  // keys held in shared memory at most (160 KB)
 
 struct EvictArgs {
     hq_kv8_t c;
@@ -137,7 +140,8 @@ struct EvictArgs {
     float* out_w;
     int64_t ob, oh;
     int32_t* idx;  // [B * heads, budget] kept slots
-    int64_t to_pages, units;
+    uint32_t to_pages, units;
+    int page_shift, keys;
     WsHeader* ws;
 };
 
@@ -151,17 +155,43 @@ __device__ __forceinline__ uint32_t weight_key(float w)
 
 __device__ __forceinline__ int64_t kept_len(const EvictArgs& a, int64_t b, bool& odd)
 {
-    const int64_t most = min(a.L, a.max_pages * a.c.page);
+    const int64_t most = min(a.L, a.max_pages << a.page_shift);
     const int64_t n = a.lens[b];
     odd = n < 0 || n > most;
     return max((int64_t)0, min(n, most));
 }
 
+// exclusive prefix sum of x over the thread block in thread order; `sums` holds one value per warp
+__device__ __forceinline__ uint64_t block_before(uint64_t x, uint64_t* sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t t = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += t;
+    }
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    if (warp == 0) {
+        uint64_t w = sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t t = __shfl_up_sync(0xFFFFFFFFu, w, o);
+            if (lane >= o) w += t;
+        }
+        sums[lane] = w;
+    }
+    __syncthreads();
+    return s - x + (warp ? sums[warp - 1] : 0ull);
+}
+
 __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a)
 {
-    __shared__ uint32_t hist[256];
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t hist[kEBins];
     __shared__ uint32_t s_digit, s_need;
-    __shared__ uint64_t warp_sum[32];
+    __shared__ uint64_t sums[kEThreads / 32];
     const int h = blockIdx.x % a.c.heads;
     const int64_t b = blockIdx.x / a.c.heads;
     bool odd;
@@ -178,132 +208,183 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
         return;
     }
     const int recent = (int)min(a.recent, (int64_t)keep);
-    const int old = n - recent;
+    const int old = n - recent, held = min(old, a.keys);
+    auto key_at = [&](int i) { return i < held ? keys[i] : weight_key(w[i]); };
+    for (int i = threadIdx.x; i < kEBins; i += kEThreads) hist[i] = 0u;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < held; i += kEThreads) keys[i] = weight_key(w[i]);
     uint32_t need = (uint32_t)(keep - recent);  // still to find at or below the digits fixed so far
-    uint32_t key = 0, mask = 0;
+    uint32_t key = 0xFFFFFFFFu;                 // need 0: nothing lies above, none is taken at it
+    __syncthreads();
     if (need > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (threadIdx.x < 256) hist[threadIdx.x] = 0u;
-            __syncthreads();
+        key = 0;
+        uint32_t mask = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+            const uint32_t digits = pass == 2 ? 1023u : 2047u;
             for (int i = threadIdx.x; i < old; i += kEThreads) {
-                const uint32_t k = weight_key(w[i]);
-                if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+                const uint32_t k = key_at(i);
+                if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & digits], 1u);
             }
             __syncthreads();
-            if (threadIdx.x == 0) {  // from the largest digit down
-                uint32_t left = need;
-                int d = 255;
-                while (d > 0 && hist[d] < left) left -= hist[d--];
-                s_digit = (uint32_t)d;
-                s_need = left;
+            // thread t owns digits 2047 - 2 t and 2046 - 2 t: the scan runs from the largest down
+            const uint32_t d = kEBins - 1 - 2 * threadIdx.x, h0 = hist[d], h1 = hist[d - 1];
+            const uint32_t above = (uint32_t)block_before(h0 + h1, sums);
+            if (above < need && need <= above + h0 + h1) {
+                const bool first = need <= above + h0;
+                s_digit = first ? d : d - 1;
+                s_need = need - above - (first ? 0u : h0);
             }
+            hist[d] = 0u;
+            hist[d - 1] = 0u;
             __syncthreads();
             key |= s_digit << shift;
-            mask |= 255u << shift;
+            mask |= digits << shift;
             need = s_need;
         }
-    } else {
-        key = 0xFFFFFFFFu;  // nothing above, none taken at
     }
     // counts of this thread's run: slots above the dividing key (high word), at it (low word)
     const int run = (old + kEThreads - 1) / kEThreads;
     const int i0 = min(old, (int)threadIdx.x * run), i1 = min(old, i0 + run);
     uint64_t mine = 0;
     for (int i = i0; i < i1; ++i) {
-        const uint32_t k = weight_key(w[i]);
+        const uint32_t k = key_at(i);
         mine += k > key ? (1ull << 32) : (k == key ? 1ull : 0ull);
     }
-    uint64_t before = mine;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t t = __shfl_up_sync(0xFFFFFFFFu, before, o);
-        if (lane >= o) before += t;
-    }
-    if (lane == 31) warp_sum[warp] = before;
-    __syncthreads();
-    before -= mine;
-    for (int i = 0; i < warp; ++i) before += warp_sum[i];
+    const uint64_t before = block_before(mine, sums);
     uint32_t above = (uint32_t)(before >> 32), at = (uint32_t)before;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = weight_key(w[i]);
-        const bool take = k > key || (k == key && at < need);
-        if (take) {
-            const uint32_t pos = above + min(at, need);
-            idx[pos] = i;
-            if (out_w) out_w[pos] = w[i];
+    if (mine)
+        for (int i = i0; i < i1; ++i) {
+            const uint32_t k = key_at(i);
+            if (k > key || (k == key && at < need)) {
+                const uint32_t pos = above + min(at, need);
+                idx[pos] = i;
+                if (out_w) out_w[pos] = w[i];
+            }
+            above += k > key;
+            at += k == key;
         }
-        above += k > key;
-        at += k == key;
-    }
     for (int i = threadIdx.x; i < recent; i += kEThreads) {
         idx[keep - recent + i] = old + i;
         if (out_w) out_w[keep - recent + i] = w[old + i];
     }
 }
 
-// Second step: one thread block per (sequence, head, new page) of keys or values gathers its rows.  The
-// page's scale is the largest of its rows' old scales; a row with a smaller one is coded again.
+// Second step: one thread block per (sequence, head, new page) gathers its rows of keys and of values.  A
+// page's scale is the largest of its rows' old scales; a row with a smaller one is coded again.  The
+// rows' places and scales are looked up once, by one thread each; then every thread has all its
+// 16-byte loads under way before the first is stored.  Bound by the scattered 64- or 128-byte rows.
 constexpr int kMThreads = 256;
 
-template <int D>
+template <int D, int PASSES>
 __global__ void __launch_bounds__(kMThreads) kv8_move_kernel(const EvictArgs a)
 {
     constexpr int LPR = D / 16, RPP = kMThreads / LPR;
-    __shared__ uint32_t s_top, s_status;
+    __shared__ int64_t s_row[128];
+    __shared__ float s_ks[128], s_vs[128];
+    __shared__ uint32_t s_top[2], s_status;
     const int page = a.c.page;
     const int sub = threadIdx.x % LPR, row = threadIdx.x / LPR;
-    if (threadIdx.x == 0) s_status = 0u, s_top = 0u;
+    if (threadIdx.x == 0) s_status = 0u, s_top[0] = 0u, s_top[1] = 0u;
     __syncthreads();
-    for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
-        const int64_t pg = u % a.to_pages;
-        const int kv = (int)(u / a.to_pages % 2);
-        const int h = (int)(u / (2 * a.to_pages) % a.c.heads);
-        const int64_t b = u / (2 * a.to_pages * a.c.heads);
+    for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x) {
+        const uint32_t bh = u / a.to_pages, pg = u - bh * a.to_pages;
+        const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * a.c.heads);
         bool odd;
         const int64_t n = min(kept_len(a, b, odd), a.budget);
         if (odd && threadIdx.x == 0) atomicOr(&s_status, kStRange);
         // out_lens may be lens itself: every reader takes min(lens, budget), the value written here
-        if (pg == 0 && kv == 0 && h == 0 && threadIdx.x == 0) a.out_lens[b] = (int32_t)n;
-        const int rows = (int)min((int64_t)page, n - pg * page);
+        if (pg == 0 && h == 0 && threadIdx.x == 0) a.out_lens[b] = (int32_t)n;
+        const int rows = (int)min((int64_t)page, n - (int64_t)pg * page);
         if (rows <= 0) continue;
-        const int32_t* idx = a.idx + (b * a.c.heads + h) * a.budget + pg * page;
-        const int32_t* table = a.table + b * a.table_stride;
         const int32_t id = a.to[b * a.to_stride + pg];
-        const uint8_t* src = kv ? a.c.v : a.c.k;
-        float* scales = kv ? a.c.v_scale : a.c.k_scale;
         bool bad = id < 0 || id >= a.c.pages;
-        uint32_t top = 0;  // positive floats order like their bit patterns
-        for (int r = threadIdx.x; r < rows; r += kMThreads) {
-            const int32_t from = table[idx[r] / page];
-            if (from < 0 || from >= a.c.pages) bad = true;
-            else top = max(top, __float_as_uint(scales[(int64_t)from * a.c.heads + h]));
+        uint32_t ktop = 0, vtop = 0;  // positive floats order like their bit patterns
+        if ((int)threadIdx.x < rows) {
+            const int32_t slot = a.idx[(int64_t)bh * a.budget + (int64_t)pg * page + threadIdx.x];
+            const int32_t from = a.table[b * a.table_stride + (slot >> a.page_shift)];
+            if (from < 0 || from >= a.c.pages) {
+                bad = true;
+            } else {
+                const int64_t ph = (int64_t)from * a.c.heads + h;
+                const float ks = a.c.k_scale[ph], vs = a.c.v_scale[ph];
+                s_row[threadIdx.x] = (ph << a.page_shift) + (slot & (page - 1));
+                s_ks[threadIdx.x] = ks;
+                s_vs[threadIdx.x] = vs;
+                ktop = __float_as_uint(ks);
+                vtop = __float_as_uint(vs);
+            }
         }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if ((threadIdx.x & 31) == 0 && top) atomicMax(&s_top, top);
+        ktop = __reduce_max_sync(0xFFFFFFFFu, ktop);
+        vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
+        if ((threadIdx.x & 31) == 0 && (ktop | vtop)) atomicMax(&s_top[0], ktop), atomicMax(&s_top[1], vtop);
         if (__syncthreads_or(bad)) {  // a page outside the pool: this page is left as it was
-            if (threadIdx.x == 0) atomicOr(&s_status, kStRange), s_top = 0u;
+            if (threadIdx.x == 0) atomicOr(&s_status, kStRange), s_top[0] = 0u, s_top[1] = 0u;
             __syncthreads();
             continue;
         }
-        const float s_to = __uint_as_float(s_top);
-        const int64_t to = ((int64_t)id * a.c.heads + h);
-        for (int r = row; r < rows; r += RPP) {
-            const int slot = idx[r];
-            const int64_t from = (int64_t)table[slot / page] * a.c.heads + h;
-            const float ratio = __fdiv_rn(scales[from], s_to);
-            uint4 q = *reinterpret_cast<const uint4*>(src + (from * page + slot % page) * D + sub * 16);
-            if (ratio != 1.0f)
-                q = make_uint4(rescale4(q.x, ratio), rescale4(q.y, ratio), rescale4(q.z, ratio), rescale4(q.w, ratio));
-            *reinterpret_cast<uint4*>((kv ? a.c.v : a.c.k) + (to * page + r) * D + sub * 16) = q;
+        const float kto = __uint_as_float(s_top[0]), vto = __uint_as_float(s_top[1]);
+        const int64_t to = (int64_t)id * a.c.heads + h;
+        uint4 q[2][PASSES];
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int r = p * RPP + row;
+            if (r < rows) {
+                const int64_t at = s_row[r] * D + sub * 16;
+                q[0][p] = *reinterpret_cast<const uint4*>(a.c.k + at);
+                q[1][p] = *reinterpret_cast<const uint4*>(a.c.v + at);
+            }
         }
-        if (threadIdx.x == 0) scales[to] = s_to;
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int r = p * RPP + row;
+            if (r < rows) {
+                const int64_t at = ((to << a.page_shift) + r) * D + sub * 16;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const float ratio = __fdiv_rn(kv ? s_vs[r] : s_ks[r], kv ? vto : kto);
+                    uint4 x = q[kv][p];
+                    if (ratio != 1.0f)
+                        x = make_uint4(rescale4(x.x, ratio), rescale4(x.y, ratio), rescale4(x.z, ratio), rescale4(x.w, ratio));
+                    *reinterpret_cast<uint4*>((kv ? a.c.v : a.c.k) + at) = x;
+                }
+            }
+        }
+        if (threadIdx.x == 0) a.c.k_scale[to] = kto, a.c.v_scale[to] = vto;
         __syncthreads();
-        if (threadIdx.x == 0) s_top = 0u;
+        if (threadIdx.x == 0) s_top[0] = 0u, s_top[1] = 0u;
         __syncthreads();
     }
     __syncthreads();
     if (threadIdx.x == 0) slot_write(a.ws, gridDim.x, blockIdx.x, s_status, 0u);
+}
+
+template <int D>
+void launch_move(const EvictArgs& a, int grid, cudaStream_t st)
+{
+    constexpr int RPP = kMThreads / (D / 16);
+    const int passes = (a.c.page + RPP - 1) / RPP;
+    if (passes == 1) kv8_move_kernel<D, 1><<<grid, kMThreads, 0, st>>>(a);
+    else if (passes == 2) kv8_move_kernel<D, 2><<<grid, kMThreads, 0, st>>>(a);
+    else kv8_move_kernel<D, 128 / RPP><<<grid, kMThreads, 0, st>>>(a);
+}
+
+template <typename T, int D>
+void launch_append_dim(const AppendArgs& a, int grid, cudaStream_t st)
+{
+    constexpr int RPP = kAThreads / (D / 8);
+    const int passes = (a.c.page + RPP - 1) / RPP;
+    if (passes == 1) kv8_append_kernel<T, D, 1><<<grid, kAThreads, 0, st>>>(a);
+    else if (passes == 2) kv8_append_kernel<T, D, 2><<<grid, kAThreads, 0, st>>>(a);
+    else if (passes == 4) kv8_append_kernel<T, D, 4><<<grid, kAThreads, 0, st>>>(a);
+    else kv8_append_kernel<T, D, 128 / RPP><<<grid, kAThreads, 0, st>>>(a);
+}
+template <typename T>
+void launch_append(const AppendArgs& a, int grid, cudaStream_t st)
+{
+    if (a.c.dim == 64) launch_append_dim<T, 64>(a, grid, st);
+    else launch_append_dim<T, 128>(a, grid, st);
 }
 
 int slots_grid(int64_t units) { return (int)(units < kMaxSlots ? units : kMaxSlots); }
@@ -345,18 +426,15 @@ extern "C" hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t 
     a.max_pages = p->max_pages;
     a.lens = p->lens;
     a.n_new = p->n_new;
-    a.span = (p->S + p->cache.page - 2) / p->cache.page + 1;
-    a.units = 2 * p->B * p->cache.heads * a.span;
+    const int64_t span = (p->S + p->cache.page - 2) / p->cache.page + 1;
+    if (span > (((int64_t)1 << 31) - 1) / (2 * p->cache.heads) / p->B) return HQ_ERR_UNSUPPORTED;
+    a.span = (uint32_t)span;
+    a.units = (uint32_t)(2 * p->B * p->cache.heads * span);
     a.ws = static_cast<WsHeader*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int grid = slots_grid(a.units);
-    if (p->dtype == HQ_BF16) {
-        if (p->cache.dim == 64) kv8_append_kernel<__nv_bfloat16, 64><<<grid, kAThreads, 0, st>>>(a);
-        else kv8_append_kernel<__nv_bfloat16, 128><<<grid, kAThreads, 0, st>>>(a);
-    } else {
-        if (p->cache.dim == 64) kv8_append_kernel<float, 64><<<grid, kAThreads, 0, st>>>(a);
-        else kv8_append_kernel<float, 128><<<grid, kAThreads, 0, st>>>(a);
-    }
+    if (p->dtype == HQ_BF16) launch_append<__nv_bfloat16>(a, grid, st);
+    else launch_append<float>(a, grid, st);
     return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
 
@@ -405,14 +483,20 @@ extern "C" hq_status_t hq_kv8_evict(const hq_kv8_evict_t* p, void* ws, size_t ws
     a.ob = p->ow_stride[0];
     a.oh = p->ow_stride[1];
     a.idx = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kSlotBytes);
-    a.to_pages = to_pages;
-    a.units = 2 * p->B * p->cache.heads * to_pages;
+    if (p->B * p->cache.heads > (((int64_t)1 << 31) - 1) / to_pages) return HQ_ERR_UNSUPPORTED;
+    a.to_pages = (uint32_t)to_pages;
+    a.units = (uint32_t)(p->B * p->cache.heads * to_pages);
+    a.page_shift = page_shift_of(p->cache.page);
+    a.keys = (int)(p->L < kEKeys ? p->L : kEKeys);
     a.ws = static_cast<WsHeader*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    kv8_select_kernel<<<(unsigned)(p->B * p->cache.heads), kEThreads, 0, st>>>(a);
+    // set on every call: the attribute belongs to the current device's context
+    if (cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(4 * kEKeys)) != cudaSuccess)
+        return HQ_ERR_CUDA;
+    kv8_select_kernel<<<(unsigned)(p->B * p->cache.heads), kEThreads, 4 * (size_t)a.keys, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return HQ_ERR_CUDA;
     const int grid = slots_grid(a.units);
-    if (p->cache.dim == 64) kv8_move_kernel<64><<<grid, kMThreads, 0, st>>>(a);
-    else kv8_move_kernel<128><<<grid, kMThreads, 0, st>>>(a);
+    if (p->cache.dim == 64) launch_move<64>(a, grid, st);
+    else launch_move<128>(a, grid, st);
     return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }

@@ -21,4 +21,6 @@ inline bool kv8_shape_supported(const hq_kv8_t* c)
     return (c->dim == 64 || c->dim == 128) && (c->page == 16 || c->page == 32 || c->page == 64 || c->page == 128);
 }
 
+inline int page_shift_of(int page) { return page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7)); }
+
 }  // namespace hq

@@ -710,7 +710,7 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     a.Hq = (int)p->Hq;
     a.Sq = (int)p->Sq;
     a.G = (int)G;
-    a.page_shift = page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7));
+    a.page_shift = page_shift_of(p->cache.page);
     a.table = p->table;
     a.table_stride = p->table_stride;
     a.slots = slots;
