@@ -57,6 +57,47 @@ struct F8Args {
     WsHeader* ws;
 };
 
+// columns n0 .. n0 + 31 of row m
+__device__ __forceinline__ void store_row32(const F8Args& a, int64_t m, int64_t n0, const float2 (&acc)[16])
+{
+    if (n0 >= a.N) return;
+    const int left = (int)(a.N - n0 < 32 ? a.N - n0 : 32);
+    if (a.bf16) {
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + m * a.N + n0;
+        if (a.vec && left == 32) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c + j].x, acc[c + j].y);
+                    w[j] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+                *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                if (2 * c < left) y[2 * c] = __float2bfloat16_rn(acc[c].x);
+                if (2 * c + 1 < left) y[2 * c + 1] = __float2bfloat16_rn(acc[c].y);
+            }
+        }
+    } else {
+        float* y = static_cast<float*>(a.Y) + m * a.N + n0;
+        if (a.vec && left == 32) {
+#pragma unroll
+            for (int c = 0; c < 16; c += 2)
+                *reinterpret_cast<float4*>(y + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                if (2 * c < left) y[2 * c] = acc[c].x;
+                if (2 * c + 1 < left) y[2 * c + 1] = acc[c].y;
+            }
+        }
+    }
+}
+
 template <int GN>
 __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
     gemm_fp8_kernel(const F8Args a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB)
@@ -176,42 +217,7 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
                     acc[c] = __ffma2_rn(make_float2(__uint_as_float(S[2 * c]), __uint_as_float(S[2 * c + 1])), ff, acc[c]);
                 f = nsa * nsw;
             }
-            if (!alive || m >= a.M || !some) continue;
-            const int left = (int)(a.N - n0 < 32 ? a.N - n0 : 32);
-            if (a.bf16) {
-                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + m * a.N + n0;
-                if (a.vec && left == 32) {
-#pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c + j].x, acc[c + j].y);
-                            w[j] = *reinterpret_cast<const uint32_t*>(&x);
-                        }
-                        *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        if (2 * c < left) y[2 * c] = __float2bfloat16_rn(acc[c].x);
-                        if (2 * c + 1 < left) y[2 * c + 1] = __float2bfloat16_rn(acc[c].y);
-                    }
-                }
-            } else {
-                float* y = static_cast<float*>(a.Y) + m * a.N + n0;
-                if (a.vec && left == 32) {
-#pragma unroll
-                    for (int c = 0; c < 16; c += 2)
-                        *reinterpret_cast<float4*>(y + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        if (2 * c < left) y[2 * c] = acc[c].x;
-                        if (2 * c + 1 < left) y[2 * c + 1] = acc[c].y;
-                    }
-                }
-            }
+            if (alive && m < a.M) store_row32(a, m, n0, acc);
         }
     }
     tc_fence_before();
@@ -219,6 +225,180 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tbase, 512);
     if (threadIdx.x == 0) slot_write(a.ws, gridDim.x, blockIdx.x, sm.status, 0u);
+}
+
+// ------------------------------------------------------------------------------------------------
+// The same product on pairs of CTAs, for outputs of many tiles: one MMA makes 256 x 256 of Y, each CTA
+// holding 128 rows of A, 128 rows of W and 128 x 256 sums, so an operand byte brought from L2 feeds
+// twice the multiplications of the 128 x 128 tile, whose operand stream (32 KB a block and CTA) is
+// what bounds it.  Eight epilogue warps of 128 columns each keep their sums in registers.
+// ------------------------------------------------------------------------------------------------
+constexpr int PN = 256, PSTAGES = 6, PACC = 2, PEPI = 8, PTHREADS = 128 + 32 * PEPI;
+// registers a thread: 384 threads start with 168; the first warpgroup (producer, MMA issuer, two idle
+// warps) gives 144 each back, which the epilogue warpgroups take 72 each of (sums 128, a TMEM load 32)
+constexpr int PREGS_LOW = 24, PREGS_HIGH = 240;
+
+struct PairSmem {
+    alignas(1024) uint8_t a[PSTAGES][GM * GK];
+    alignas(1024) uint8_t b[PSTAGES][GM * GK];
+    alignas(8) uint64_t full[PSTAGES];
+    uint64_t empty[PSTAGES];
+    uint64_t acc_full[PACC];
+    uint64_t acc_empty[PACC];
+    uint32_t tmem_base;
+    uint32_t status;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
+    gemm_fp8_pair_kernel(const F8Args a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    PairSmem& sm = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int KB = (int)((a.K + GK - 1) / GK);
+    const int NT = (int)((a.N + PN - 1) / PN);
+    const int64_t tiles = ((a.M + 2 * GM - 1) / (2 * GM)) * NT;
+    const int64_t tile0 = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < PSTAGES; ++s) {
+            mbar_init(&sm.full[s], 1);   // even CTA: its own arrival and both CTAs' bytes
+            mbar_init(&sm.empty[s], 1);  // the MMAs' commit, in both CTAs
+        }
+        for (int s = 0; s < PACC; ++s) {
+            mbar_init(&sm.acc_full[s], 1);
+            mbar_init(&sm.acc_empty[s], 2 * PEPI);  // even CTA: both CTAs' epilogue warps
+        }
+        sm.status = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc2(&sm.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tbase = sm.tmem_base;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PREGS_LOW));
+        if (warp == 0 && lane == 0) {
+            int it = 0;
+            bool alive = true;
+            for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
+                const int m0 = (int)(tile / NT) * 2 * GM + (int)rank * GM, n0 = (int)(tile % NT) * PN + (int)rank * GM;
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const int s = it % PSTAGES;
+                    if (it >= PSTAGES && !mbar_wait_sleep(&sm.empty[s], (uint32_t)((it / PSTAGES - 1) & 1))) {
+                        atomicOr(&sm.status, kStTimeout);
+                        alive = false;
+                        break;
+                    }
+                    const uint32_t bar = peer_addr(&sm.full[s], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4u * GM * GK);
+                    tma_load_2d_pair(sm.a[s], &tA, kb * GK, m0, bar);
+                    tma_load_2d_pair(sm.b[s], &tB, kb * GK, n0, bar);
+                }
+            }
+            // no copy of either CTA may be in flight when the pair leaves
+            if (rank == 0)
+                for (int j = it > PSTAGES ? it - PSTAGES : 0; j < it; ++j)
+                    mbar_wait_sleep(&sm.full[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            int it = 0;
+            bool alive = true;
+            for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const int s = it % PSTAGES, slot = it % PACC;
+                    if ((it >= PACC && !mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / PACC - 1) & 1))) ||
+                        !mbar_wait_sleep(&sm.full[s], (uint32_t)((it / PSTAGES) & 1))) {
+                        atomicOr(&sm.status, kStTimeout);
+                        alive = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = sw128_desc(sm.a[s]), bd = sw128_desc(sm.b[s]);
+#pragma unroll
+                    for (int kk = 0; kk < GK / 32; ++kk)
+                        mma_f8_pair(tbase + (uint32_t)(slot * PN), ad + (uint64_t)(2 * kk), bd + (uint64_t)(2 * kk),
+                                    idesc_f8(2 * GM, PN), kk > 0 ? 1u : 0u);
+                    mma_commit_pair(&sm.empty[s]);
+                    mma_commit_pair(&sm.acc_full[slot]);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PREGS_HIGH));
+        // warpgroup h takes columns 128 h .. 128 h + 127 of each slot: one scale of W
+        const int q = warp & 3, h = (warp - 4) >> 2, row = q * 32 + lane;
+        const int64_t NB = (a.N + 127) / 128;
+        int it = 0;
+        bool alive = true;
+        for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
+            const int64_t m = (tile / NT) * 2 * GM + rank * GM + row, n0 = (tile % NT) * PN + 128 * h;
+            const float* sa = a.sa + (m < a.M ? m : 0);
+            const float* sw = a.sw + n0 / 128;
+            const bool some = n0 < a.N;
+            float2 acc[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
+            float f = some ? __ldg(sa) * __ldg(sw) : 0.0f;
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int slot = it % PACC;
+                const float nsa = some && kb + 1 < KB ? __ldg(sa + (int64_t)(kb + 1) * a.M) : 0.0f;
+                const float nsw = some && kb + 1 < KB ? __ldg(sw + (int64_t)(kb + 1) * NB) : 0.0f;
+                const bool got = mbar_wait_sleep(&sm.acc_full[slot], (uint32_t)((it / PACC) & 1));
+                __syncwarp();
+                if (!__all_sync(0xFFFFFFFFu, got)) {
+                    if (lane == 0) atomicOr(&sm.status, kStTimeout);
+                    alive = false;
+                    break;
+                }
+                tc_fence_after();
+                const float2 ff = make_float2(f, f);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    uint32_t S[32];
+                    tmem_ld32_nowait(tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * PN + 128 * h + 32 * p), S);
+                    tmem_wait_ld();
+                    if (p == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(peer_addr(&sm.acc_empty[slot], 0));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        acc[16 * p + c] =
+                            __ffma2_rn(make_float2(__uint_as_float(S[2 * c]), __uint_as_float(S[2 * c + 1])), ff, acc[16 * p + c]);
+                }
+                f = nsa * nsw;
+            }
+            if (!alive || m >= a.M) continue;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float2(&part)[16] = *reinterpret_cast<const float2(*)[16]>(&acc[16 * p]);
+                store_row32(a, m, n0 + 32 * p, part);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the other's MMAs, commits or arrivals may reach it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc2(tbase, 512);
+    if (threadIdx.x == 0) slot_write(a.ws, gridDim.x, blockIdx.x, sm.status, 0u);
+}
+
+cudaError_t launch_gemm_fp8_pair(const F8Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st)
+{
+    const size_t smem = sizeof(PairSmem) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ((a.M + 2 * GM - 1) / (2 * GM)) * ((a.N + PN - 1) / PN);
+    const int pairs = (int)(tiles < num_sms() / 2 ? tiles : num_sms() / 2);
+    gemm_fp8_pair_kernel<<<2 * pairs, PTHREADS, smem, st>>>(a, ta, tb);
+    return cudaGetLastError();
 }
 
 template <int GN>
@@ -252,15 +432,17 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
     DeviceGuard dev(A);
     if (!dev.ok) return HQ_ERR_ARG;
     const int64_t sms = num_sms(), mt = (M + GM - 1) / GM;
+    const bool pair = ((M + 2 * GM - 1) / (2 * GM)) * ((N + PN - 1) / PN) >= sms / 2;
     int gn = 128;  // the widest tile whose tiles occupy every SM, 32 columns if none does
     while (gn > 32 && mt * ((N + gn - 1) / gn) < sms) gn /= 2;
     // K blocks over all tiles of a CTA are counted in 31 bits
     if ((mt * ((N + gn - 1) / gn) / sms + 1) * ((K + GK - 1) / GK) > ((int64_t)1 << 30)) return HQ_ERR_UNSUPPORTED;
     CUtensorMap ta, tb;
-    if (!tensor_map_bytes(&ta, A, M, K, lda, GM) || !tensor_map_bytes(&tb, W, N, K, ldw, gn)) return HQ_ERR_CUDA;
+    if (!tensor_map_bytes(&ta, A, M, K, lda, GM) || !tensor_map_bytes(&tb, W, N, K, ldw, pair ? GM : gn)) return HQ_ERR_CUDA;
     F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, static_cast<WsHeader*>(ws)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = gn == 128 ? launch_gemm_fp8<128>(a, ta, tb, st)
+    const cudaError_t e = pair        ? launch_gemm_fp8_pair(a, ta, tb, st)
+                          : gn == 128 ? launch_gemm_fp8<128>(a, ta, tb, st)
                                     : (gn == 64 ? launch_gemm_fp8<64>(a, ta, tb, st) : launch_gemm_fp8<32>(a, ta, tb, st));
     return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
