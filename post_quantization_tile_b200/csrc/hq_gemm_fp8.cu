@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
 // twice the multiplications of the 128 x 128 tile, whose operand stream (32 KB a block and CTA) is
 // what bounds it.  Eight epilogue warps of 128 columns each keep their sums in registers.
 // ------------------------------------------------------------------------------------------------
-constexpr int PN = 256, PSTAGES = 6, PACC = 2, PEPI = 8, PTHREADS = 128 + 32 * PEPI;
+constexpr int PN = 256, PSTAGES = 5, PACC = 2, PEPI = 8, PTHREADS = 128 + 32 * PEPI;
 // registers a thread: 384 threads start with 168; the first warpgroup (producer, MMA issuer, two idle
 // warps) gives 144 each back, which the epilogue warpgroups take 72 each of (sums 128, a TMEM load 32)
 constexpr int PREGS_LOW = 24, PREGS_HIGH = 240;
@@ -241,6 +241,7 @@ constexpr int PREGS_LOW = 24, PREGS_HIGH = 240;
 struct PairSmem {
     alignas(1024) uint8_t a[PSTAGES][GM * GK];
     alignas(1024) uint8_t b[PSTAGES][GM * GK];
+    alignas(128) uint8_t out[PEPI][32 * 128];  // 128 bytes of each of a warp's rows on their way to Y
     alignas(8) uint64_t full[PSTAGES];
     uint64_t empty[PSTAGES];
     uint64_t acc_full[PACC];
@@ -344,37 +345,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.0f, 0.0f);
             float f = some ? __ldg(sa) * __ldg(sw) : 0.0f;
-            for (int kb = 0; kb < KB; ++kb, ++it) {
+            const uint32_t ta = tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(128 * h);
+            // 32 columns are on their way from TMEM while the 32 before them are scaled, across blocks too
+            uint32_t S[2][32];
+            auto await_block = [&](int i) {
+                const bool got = mbar_wait_sleep(&sm.acc_full[i % PACC], (uint32_t)((i / PACC) & 1));
+                __syncwarp();
+                if (__all_sync(0xFFFFFFFFu, got)) {
+                    tc_fence_after();
+                    tmem_ld32_nowait(ta + (uint32_t)((i % PACC) * PN), S[0]);
+                    return true;
+                }
+                if (lane == 0) atomicOr(&sm.status, kStTimeout);
+                return false;
+            };
+            alive = await_block(it);
+            for (int kb = 0; alive && kb < KB; ++kb, ++it) {
                 const int slot = it % PACC;
                 const float nsa = some && kb + 1 < KB ? __ldg(sa + (int64_t)(kb + 1) * a.M) : 0.0f;
                 const float nsw = some && kb + 1 < KB ? __ldg(sw + (int64_t)(kb + 1) * NB) : 0.0f;
-                const bool got = mbar_wait_sleep(&sm.acc_full[slot], (uint32_t)((it / PACC) & 1));
-                __syncwarp();
-                if (!__all_sync(0xFFFFFFFFu, got)) {
-                    if (lane == 0) atomicOr(&sm.status, kStTimeout);
-                    alive = false;
-                    break;
-                }
-                tc_fence_after();
                 const float2 ff = make_float2(f, f);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
-                    uint32_t S[32];
-                    tmem_ld32_nowait(tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * PN + 128 * h + 32 * p), S);
                     tmem_wait_ld();
-                    if (p == 3) {
+                    if (p < 3) {
+                        tmem_ld32_nowait(ta + (uint32_t)(slot * PN + 32 * (p + 1)), S[(p + 1) & 1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(peer_addr(&sm.acc_empty[slot], 0));
+                        if (kb + 1 < KB) alive = await_block(it + 1);
                     }
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        acc[16 * p + c] =
-                            __ffma2_rn(make_float2(__uint_as_float(S[2 * c]), __uint_as_float(S[2 * c + 1])), ff, acc[16 * p + c]);
+                        acc[16 * p + c] = __ffma2_rn(
+                            make_float2(__uint_as_float(S[p & 1][2 * c]), __uint_as_float(S[p & 1][2 * c + 1])), ff, acc[16 * p + c]);
                 }
                 f = nsa * nsw;
             }
-            if (!alive || m >= a.M) continue;
+            if (!alive) continue;
+            if (a.vec && n0 + 128 <= a.N) {
+                // through shared memory, so that a warp stores 128 contiguous bytes of four rows at a time
+                uint8_t* out = sm.out[warp - 4];
+                const int es = a.bf16 ? 2 : 4;
+                const int64_t r0 = m - lane;
+                uint8_t* y = static_cast<uint8_t*>(a.Y) + (r0 * a.N + n0) * es;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if (a.bf16 && (p & 1)) continue;
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint4 w;
+                        if (a.bf16) {
+                            const float2* v = &acc[16 * (p & 2) + 4 * j];
+                            const __nv_bfloat162 x0 = __floats2bfloat162_rn(v[0].x, v[0].y), x1 = __floats2bfloat162_rn(v[1].x, v[1].y);
+                            const __nv_bfloat162 x2 = __floats2bfloat162_rn(v[2].x, v[2].y), x3 = __floats2bfloat162_rn(v[3].x, v[3].y);
+                            w = make_uint4(*reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1),
+                                           *reinterpret_cast<const uint32_t*>(&x2), *reinterpret_cast<const uint32_t*>(&x3));
+                        } else {
+                            const float2* v = &acc[16 * p + 2 * j];
+                            w = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                                           __float_as_uint(v[1].y));
+                        }
+                        *reinterpret_cast<uint4*>(out + swz(lane, j)) = w;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = 4 * k + (lane >> 3);
+                        if (r0 + r < a.M)
+                            *reinterpret_cast<uint4*>(y + (int64_t)r * a.N * es + 32 * p * es + (lane & 7) * 16) =
+                                *reinterpret_cast<const uint4*>(out + swz(r, lane & 7));
+                    }
+                }
+                continue;
+            }
+            if (m >= a.M) continue;
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const float2(&part)[16] = *reinterpret_cast<const float2(*)[16]>(&acc[16 * p]);
