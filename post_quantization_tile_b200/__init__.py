@@ -120,7 +120,7 @@ def lib():
         L.hq_gemm_fp8.argtypes = [P, i64, P, i64, P, i64, P, i64, i64, P, i32, P, ctypes.c_size_t, P]
         for f in ("hq_kv8_append", "hq_kv8_attend", "hq_kv8_evict"):  # a packed argument struct, ws, stream
             getattr(L, f).argtypes = [ctypes.c_char_p, P, ctypes.c_size_t, P]
-        L.hq_kv8_attend_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+        L.hq_kv8_attend_workspace_bytes.argtypes = [i64, i32, i64, i64, i32, i32]
         L.hq_kv8_attend_workspace_bytes.restype = ctypes.c_size_t
         L.hq_kv8_evict_workspace_bytes.argtypes = [i64, i32, i64]
         L.hq_kv8_evict_workspace_bytes.restype = ctypes.c_size_t
@@ -605,7 +605,8 @@ def _scratch(ws: Workspace | None, need: int, dev: torch.device):
 
 
 def _raw_stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    """The current stream of the tensors' device (torch.cuda.current_stream builds an object first)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _on(dev: torch.device, t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, contiguous: bool = True) -> int:
@@ -756,8 +757,8 @@ def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
 
 
 @functools.lru_cache(maxsize=256)
-def _attend_bytes(B: int, Hq: int, Sq: int, D: int, weights: int) -> int:
-    return lib().hq_kv8_attend_workspace_bytes(B, Hq, Sq, D, weights)
+def _attend_bytes(B: int, heads: int, Hq: int, Sq: int, D: int, weights: int) -> int:
+    return lib().hq_kv8_attend_workspace_bytes(B, heads, Hq, Sq, D, weights)
 
 
 def kv8_attend(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor,
@@ -802,7 +803,7 @@ def kv8_attend(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torc
             raise ValueError("weights need a contiguous last dimension")
     elif weights_in is not None:
         raise ValueError("weights_in without weights")
-    wp, wn, _keep = _scratch(ws, _attend_bytes(B, Hq, Sq, D, weights is not None), dev)
+    wp, wn, _keep = _scratch(ws, _attend_bytes(B, head[5], Hq, Sq, D, weights is not None), dev)
     arg = _KV8_ATTEND.pack(head[0], head[1], head[2], head[3], head[4], head[5], head[6], head[7], q.data_ptr(), out.data_ptr(),
                            B, Hq, Sq, qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], tp, tstride, P,
                            _on(dev, lens, "lens", torch.int32, (B,)),

@@ -24,12 +24,12 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-li
          # no contraction: the encode chain is specified in binary32 without fused multiply-add
          "-fmad=false", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2", "--expt-relaxed-constexpr"]
 SOURCES = ["hq_api.cu", "hq_noalloc.cu", "hq_gemm.cu", "hq_gemm_code.cu", "hq_dense.cu", "hq_fp8.cu",
-           "hq_gemm_fp8.cu", "hq_kv8.cu", "hq_kv8_attend.cu", "hq_inst_z.cu", "hq_inst_a2.cu", "hq_inst_d4.cu",
+           "hq_gemm_fp8.cu", "hq_kv8.cu", "hq_kv8_attend.cu", "hq_kv8_prefill.cu", "hq_inst_z.cu", "hq_inst_a2.cu", "hq_inst_d4.cu",
            "hq_inst_e8.cu"]
 # sources compiled a second time with the test hooks for libhq_test.so
 TEST_SOURCES = ["hq_api.cu", "hq_inst_e8.cu"]
 HEADERS = ["hq_common.cuh", "hq_tc.cuh", "hq_lattice.cuh", "hq_encode.cuh", "hq_decode.cuh", "hq_instantiate.cuh", "hq_launch.h",
-           "hq_fp8.cuh", "hq_kv8.cuh"]
+           "hq_fp8.cuh", "hq_kv8.cuh", "hq_kv8_attend.cuh"]
 
 
 def _newest_dep() -> float:

@@ -25,59 +25,38 @@
 //     units of the last value scale and multiplied by the (power-of-two) ratio when that changes.
 #include <cuda_runtime.h>
 
-#include "hq_kv8.cuh"
+#include "hq_kv8_attend.cuh"
 
 namespace hq {
 namespace {
 
 constexpr int kWarps = 4, kThreadsA = 32 * kWarps;
-constexpr int kTile = 64;         // tokens of one share unit
-constexpr int kMaxBatch = 4096;   // sequences of one call (their prefix sums live in shared memory)
-constexpr int kMaxGrid = 512;
-constexpr int kStages = 4;        // ring of sixteen-token groups per warp
-constexpr float kBoost = 7.0f;    // probabilities are held times 2^7, and up to 2^8 times that
-constexpr float kSlack = 8.0f;    // before a larger maximum moves the reference they are relative to
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kStages = 4;  // ring of sixteen-token groups per warp
 
-struct AttendArgs {
-    hq_kv8_t c;
-    const __nv_bfloat16* q;
-    int64_t qb, qh, qs;
-    __nv_bfloat16* out;
-    int64_t ob, oh, os;
-    int B, Hq, Sq, G, page_shift;
-    const int32_t* table;
-    int64_t table_stride;
-    int64_t slots;  // max_pages * page
-    const int32_t* lens;
-    const int32_t* q_lens;
-    float scale;
-    int causal;
-    float* lse;
-    int64_t lb, lh;
-    const float* win;
-    float* w;
-    int64_t wib, wih, wb, wh, L;
-    uint32_t* prefix;  // [B + 1] share units before each sequence
-    float* part_o;     // [2 grid][16][D]
-    float2* part_ml;   // [2 grid][16]
-    float* lse2;       // [B][heads][G Sq] binary logarithm of the sums (weights only)
-    WsHeader* ws;
+// units of sixteen rows in tiles of 64 slots; slots that only later rows of a sequence see are part of
+// every unit's tiles (at most its queries: few) and skipped
+struct FewRows {
+    static constexpr int R = 16, TILE = 64;
+    static __device__ __forceinline__ int row_tiles(const AttendArgs& a, int m) { return (m * a.G + R - 1) / R; }
+    static __device__ __forceinline__ uint32_t tiles(const AttendArgs&, const SeqLen& s, int) { return (uint32_t)((s.n + TILE - 1) / TILE); }
+    static __device__ __forceinline__ uint32_t of_sequence(const AttendArgs& a, const SeqLen& s)
+    {
+        return (uint32_t)(a.c.heads * row_tiles(a, s.m)) * tiles(a, s, 0);
+    }
+    static __device__ __forceinline__ uint32_t before(const AttendArgs& a, const SeqLen& s, int h, int rt)
+    {
+        return (uint32_t)(h * row_tiles(a, s.m) + rt) * tiles(a, s, 0);
+    }
+    static __device__ __forceinline__ void find(const AttendArgs& a, const SeqLen& s, uint32_t, uint32_t at, Segment& g)
+    {
+        const int rts = row_tiles(a, s.m);
+        g.tiles = tiles(a, s, 0);
+        const uint32_t unit = at / g.tiles;
+        g.t0 = at - unit * g.tiles;
+        g.h = unit / rts;
+        g.rt = unit - g.h * rts;
+    }
 };
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -85,27 +64,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// lengths of sequence b: cached slots and queries, inside what the call's shapes allow
-struct SeqLen {
-    int n, m;
-    bool odd;
-};
-__device__ __forceinline__ SeqLen seq_len(const AttendArgs& a, int b)
-{
-    SeqLen s;
-    const int n = a.lens[b], m = a.q_lens ? a.q_lens[b] : a.Sq;
-    s.n = (int)max((int64_t)0, min((int64_t)n, a.slots));
-    s.m = max(0, min(m, a.Sq));
-    s.odd = n != s.n || m != s.m || (a.w && s.n > a.L);
-    return s;
-}
-__device__ __forceinline__ int row_tiles(const AttendArgs& a, int m) { return (m * a.G + 15) / 16; }
-// slots that query i of m sees, of n
-__device__ __forceinline__ int sees(const AttendArgs& a, int n, int m, int i)
-{
-    return a.causal ? max(0, n - m + i + 1) : n;
 }
 
 // sixteen query rows as the A fragments of the score product, and the factors of their scores
@@ -235,14 +193,6 @@ struct ValueGroup {
     }
 };
 
-// first cache row (of [page][head][token]) of sixteen tokens from slot `tok`; -1 if their page is
-// outside the pool.  The entry points keep the number of rows below 2^31.
-__device__ __forceinline__ int locate(const AttendArgs& a, const int32_t* table, int h, int tok)
-{
-    const int32_t id = __ldg(table + (tok >> a.page_shift));
-    return id >= 0 && id < a.c.pages ? (int)(((uint32_t)id * a.c.heads + h) << a.page_shift) + (tok & (a.c.page - 1)) : -1;
-}
-
 template <int D>
 struct AttendSmem {
     unsigned char ring[kWarps][kStages][2][16 * D];  // keys, values of a group (TMA boxes: 1024-byte aligned)
@@ -253,21 +203,6 @@ struct AttendSmem {
     uint32_t scan[kWarps];
     uint32_t status;
 };
-
-// a finished row r of a unit: the output, the logarithm of its sum
-__device__ __forceinline__ void row_place(const AttendArgs& a, int h, int r, int& head, int& i)
-{
-    i = r / a.G;
-    head = h * a.G + (r - i * a.G);
-}
-__device__ __forceinline__ void write_lse(const AttendArgs& a, int b, int h, int r, float M, float l)
-{
-    int head, i;
-    row_place(a, h, r, head, i);
-    const float l2 = l > 0.0f ? M - kBoost + log2f(l) : (l == 0.0f ? -INFINITY : l);  // a NaN sum stays one
-    if (a.lse) a.lse[b * a.lb + head * a.lh + i] = l2 * kLn2;
-    if (a.lse2) a.lse2[((int64_t)b * a.c.heads + h) * a.G * a.Sq + r] = l2;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsA, 2)
@@ -283,37 +218,7 @@ __global__ void __launch_bounds__(kThreadsA, 2)
             for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[w][i], 1);
         fence_mbar_init();
     }
-    // prefix sums of the sequences' share units
-    {
-        const int run = (a.B + kThreadsA - 1) / kThreadsA, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
-        uint32_t mine = 0;
-        bool odd = false;
-        for (int b = b0; b < b1; ++b) {
-            const SeqLen s = seq_len(a, b);
-            odd |= s.odd;
-            mine += (uint32_t)(a.c.heads * row_tiles(a, s.m)) * (uint32_t)((s.n + kTile - 1) / kTile);
-        }
-        uint32_t inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += x;
-        }
-        if (lane == 31) sm.scan[warp] = inc;
-        __syncthreads();
-        uint32_t at = inc - mine;
-        for (int i = 0; i < warp; ++i) at += sm.scan[i];
-        for (int b = b0; b < b1; ++b) {
-            pre[b] = at;
-            const SeqLen s = seq_len(a, b);
-            at += (uint32_t)(a.c.heads * row_tiles(a, s.m)) * (uint32_t)((s.n + kTile - 1) / kTile);
-        }
-        if (tid == kThreadsA - 1) pre[a.B] = at;
-        if (odd && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
-        __syncthreads();
-        if (blockIdx.x == 0)
-            for (int b = tid; b <= a.B; b += kThreadsA) a.prefix[b] = pre[b];
-    }
+    if (share_prefix<FewRows, kThreadsA>(a, pre, sm.scan) && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
     const uint32_t W = pre[a.B];
     const uint32_t shares = min(W, gridDim.x);  // none is empty: the join walks a unit's shares one by one
     uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
@@ -322,21 +227,12 @@ __global__ void __launch_bounds__(kThreadsA, 2)
     bool dead = false;  // after a timeout a warp only walks the loops, so that all reach the barriers
     uint32_t it = 0;  // groups this warp has issued before this unit: ring stage and parity
     while (w0 < w1) {
-        // the unit that share unit w0 belongs to
-        int b = 0;
-        for (int hi = a.B; hi - b > 1;) {
-            const int mid = (b + hi) >> 1;
-            if (pre[mid] <= w0) b = mid;
-            else hi = mid;
-        }
-        const SeqLen s = seq_len(a, b);
-        const uint32_t tiles = (uint32_t)((s.n + kTile - 1) / kTile);
-        const int rts = row_tiles(a, s.m);
-        const uint32_t unit = (w0 - pre[b]) / tiles, t0 = (w0 - pre[b]) % tiles;
-        const uint32_t t1 = min(tiles, t0 + (w1 - w0));
-        const int h = unit / rts, rt = unit % rts;
+        const Segment seg = segment_at<FewRows>(a, pre, w0, w1);
+        const SeqLen s = seg.s;
+        const int b = seg.b, h = seg.h, rt = seg.rt;
+        const uint32_t t0 = seg.t0, t1 = seg.t1, tiles = seg.tiles;
         const int last_row = min(rt * 16 + 15, s.m * a.G - 1);
-        const int end = min((int)t1 * kTile, sees(a, s.n, s.m, last_row / a.G));
+        const int end = min((int)t1 * FewRows::TILE, sees(a, s.n, s.m, last_row / a.G));
         const int groups = (end + 15) / 16;  // sixteen-token groups up to the last visible slot
         const int32_t* table = a.table + b * a.table_stride;
 
@@ -349,7 +245,7 @@ __global__ void __launch_bounds__(kThreadsA, 2)
 
         // this warp's groups: every kWarps-th; their page rows and scales are fetched 32 at a time, one
         // per lane, and the boxes of kStages groups are under way at any time
-        const int gr0 = (int)t0 * (kTile / 16) + warp, count = gr0 < groups && !dead ? (groups - gr0 + kWarps - 1) / kWarps : 0;
+        const int gr0 = (int)t0 * (FewRows::TILE / 16) + warp, count = gr0 < groups && !dead ? (groups - gr0 + kWarps - 1) / kWarps : 0;
         int my_row = -1;
         float2 my_scale = make_float2(0.0f, -1.0f);
         auto issue = [&](int i) {
@@ -518,53 +414,6 @@ __global__ void __launch_bounds__(kThreadsA, 2)
     if (tid == 0) slot_write(a.ws, gridDim.x, blockIdx.x, sm.status, 0u);
 }
 
-// joins the parts of the units that were cut, and writes zeros where a row sees nothing
-template <int D>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
-{
-    const int rt = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
-    const int h = bh % a.c.heads, b = bh / a.c.heads;
-    const SeqLen s = seq_len(a, b);
-    const int rts = row_tiles(a, s.m);
-    if (rt >= rts) return;
-    const uint32_t tiles = (uint32_t)((s.n + kTile - 1) / kTile), W = a.prefix[a.B];
-    const uint32_t w0 = a.prefix[b] + ((uint32_t)h * rts + rt) * tiles, w1 = w0 + tiles;
-    // the share that holds share unit w: the smallest c with w < floor((c + 1) W / shares)
-    const uint32_t shares = min(W, (uint32_t)grid);
-    const int c0 = tiles ? (int)(((uint64_t)(w0 + 1) * shares - 1) / W) : 0;
-    const int c1 = tiles ? (int)(((uint64_t)w1 * shares - 1) / W) : 0;
-    if (tiles && c0 == c1) return;  // whole: written already
-    constexpr int TPR = 8, DPT = D / TPR;
-    const int r = threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * DPT, rr = rt * 16 + r;
-    if (rr >= s.m * a.G) return;
-    float M = -INFINITY, L = 0.0f, y[DPT];
-#pragma unroll
-    for (int d = 0; d < DPT; ++d) y[d] = 0.0f;
-    if (tiles) {
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * c + (c == c0)) * 16 + r].x);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t at = (int64_t)(2 * c + (c == c0)) * 16 + r;
-            const float2 ml = a.part_ml[at];
-            const float f = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
-            L = fmaf(ml.y, f, L);
-#pragma unroll
-            for (int d = 0; d < DPT; d += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + d0 + d);
-                y[d] = fmaf(x.x, f, y[d]), y[d + 1] = fmaf(x.y, f, y[d + 1]), y[d + 2] = fmaf(x.z, f, y[d + 2]), y[d + 3] = fmaf(x.w, f, y[d + 3]);
-            }
-        }
-    }
-    if (d0 == 0) write_lse(a, b, h, rr, M, L);
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    int head, i;
-    row_place(a, h, rr, head, i);
-    __nv_bfloat16* out = a.out + b * a.ob + head * a.oh + (int64_t)i * a.os + d0;
-#pragma unroll
-    for (int d = 0; d < DPT; d += 2) *reinterpret_cast<__nv_bfloat162*>(out + d) = __floats2bfloat162_rn(y[d] * inv, y[d + 1] * inv);
-}
-
 // The weight each cached slot received, summed over a key head's rows: with the rows' sums known,
 // exp(s - lse) is recomputed from the keys.  One warp takes sixteen slots and walks the row tiles, so
 // every slot is summed by one lane group in a fixed order.
@@ -584,7 +433,7 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
     const float ks = ok ? __ldg(a.c.k_scale + (row >> a.page_shift)) : 0.0f;
     float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
     const float* lse2 = a.lse2 + ((int64_t)b * a.c.heads + h) * a.G * a.Sq;
-    const int rts = row_tiles(a, s.m);
+    const int rts = FewRows::row_tiles(a, s.m);
     for (int rt = 0; rt < rts; ++rt) {
         QueryRows<D> q;
         q.load(a, b, h, rt, s);
@@ -618,35 +467,48 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// The kernel for many rows (tensor memory, units of 256 rows) reads the cache once for all of them; this
+// one once for every sixteen, from L2.  One unit of sixteen rows: this one.
+bool many_rows(int64_t rows) { return rows > FewRows::R; }
+int attend_grid(bool many) { return many ? num_sms() : 2 * num_sms(); }
+constexpr int kMaxGridFew = 512, kMaxGridMany = 256;
+
 struct AttendLayout {
     size_t prefix, part_o, part_ml, lse2, bytes;
 };
-AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool weights)
+AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool weights, bool many)
 {
+    const size_t parts = many ? (size_t)2 * kMaxGridMany * kManyRows : (size_t)2 * kMaxGridFew * FewRows::R;
     AttendLayout l;
     l.prefix = align256(kSlotBytes);
     l.part_o = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 1));
-    l.part_ml = l.part_o + (size_t)2 * kMaxGrid * 16 * (size_t)D * sizeof(float);
-    l.lse2 = l.part_ml + (size_t)2 * kMaxGrid * 16 * sizeof(float2);
+    l.part_ml = l.part_o + parts * (size_t)D * sizeof(float);
+    l.lse2 = l.part_ml + parts * sizeof(float2);
     l.bytes = l.lse2 + (weights ? align256(sizeof(float) * (size_t)(B * Hq * Sq)) : 0);
     return l;
 }
 
 template <int D>
-cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st)
+cudaError_t launch_attend(const AttendArgs& a, bool many, cudaStream_t st)
 {
-    CUtensorMap tk, tv;
-    const int64_t rows = a.c.pages * a.c.heads * a.c.page;
-    if (!tensor_map_kv8(&tk, a.c.k, rows, D, 16) || !tensor_map_kv8(&tv, a.c.v, rows, D, 16)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + sizeof(AttendSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 1);
-    cudaError_t e = cudaFuncSetAttribute(kv8_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int grid = 2 * num_sms() < kMaxGrid ? 2 * num_sms() : kMaxGrid;
-    kv8_attend_kernel<D><<<grid, kThreadsA, smem, st>>>(a, tk, tv);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int rts = (a.Sq * a.G + 15) / 16;
-    kv8_join_kernel<D><<<(unsigned)(a.B * a.c.heads * rts), 128, 0, st>>>(a, rts, grid);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaError_t e;
+    if (many) {
+        const int grid = attend_grid(true) < kMaxGridMany ? attend_grid(true) : kMaxGridMany;
+        if ((e = launch_attend_many(a, grid, st)) != cudaSuccess) return e;
+    } else {
+        CUtensorMap tk, tv;
+        const int64_t rows = a.c.pages * a.c.heads * a.c.page;
+        if (!tensor_map_kv8(&tk, a.c.k, rows, D, 16) || !tensor_map_kv8(&tv, a.c.v, rows, D, 16)) return cudaErrorInvalidValue;
+        const size_t smem = 1024 + sizeof(AttendSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 1);
+        e = cudaFuncSetAttribute(kv8_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        const int grid = attend_grid(false) < kMaxGridFew ? attend_grid(false) : kMaxGridFew;
+        kv8_attend_kernel<D><<<grid, kThreadsA, smem, st>>>(a, tk, tv);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const int rts = (a.Sq * a.G + 15) / 16;
+        kv8_join_kernel<D, FewRows><<<(unsigned)(a.B * a.c.heads * rts), 128, 0, st>>>(a, rts, grid);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
     if (a.w) {
         const int64_t most = a.slots < a.L ? a.slots : a.L;
         const dim3 wg((unsigned)((most + 16 * kWarps - 1) / (16 * kWarps)), (unsigned)a.c.heads, (unsigned)a.B);
@@ -661,10 +523,12 @@ cudaError_t launch_attend(const AttendArgs& a, cudaStream_t st)
 
 using namespace hq;
 
-extern "C" size_t hq_kv8_attend_workspace_bytes(int64_t B, int64_t Hq, int64_t Sq, int32_t D, int32_t weights)
+extern "C" size_t hq_kv8_attend_workspace_bytes(int64_t B, int32_t heads, int64_t Hq, int64_t Sq, int32_t D, int32_t weights)
 {
-    if (B < 1 || B > kMaxBatch || Hq < 1 || Sq < 1 || (D != 64 && D != 128) || Hq > 65535 || Sq > ((int64_t)1 << 24)) return 0;
-    return attend_layout(B, Hq, Sq, D, weights != 0).bytes;
+    if (B < 1 || B > kMaxBatch || heads < 1 || Hq < heads || Hq % heads || Sq < 1 || (D != 64 && D != 128) || Hq > 65535 ||
+        Sq > ((int64_t)1 << 24))
+        return 0;
+    return attend_layout(B, Hq, Sq, D, weights != 0, many_rows(Sq * (Hq / heads))).bytes;
 }
 
 extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t ws_bytes, void* stream)
@@ -679,7 +543,7 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     if (p->cache.pages * H > (((int64_t)1 << 31) - 1) / page) return HQ_ERR_UNSUPPORTED;  // cache rows in 31 bits
     // share units and thread blocks are counted in 31 bits, slots of a sequence too
     if (slots > ((int64_t)1 << 30) || p->Sq * G > ((int64_t)1 << 26) || p->B * H > ((int64_t)1 << 26) ||
-        p->B * H * rts > ((int64_t)1 << 31) / ((slots + kTile - 1) / kTile))
+        p->B * H * rts > ((int64_t)1 << 31) / ((slots + FewRows::TILE - 1) / FewRows::TILE))
         return HQ_ERR_UNSUPPORTED;
     const int64_t qs = p->q_stride[0] | p->q_stride[1] | p->q_stride[2];
     const int64_t os = p->out_stride[0] | p->out_stride[1] | p->out_stride[2];
@@ -692,7 +556,8 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     if (p->weights && p->L < 1) return HQ_ERR_ARG;
     if (p->weights_in && !p->weights) return HQ_ERR_ARG;
     if (p->weights && p->B > 65535) return HQ_ERR_UNSUPPORTED;
-    const AttendLayout l = attend_layout(p->B, p->Hq, p->Sq, p->cache.dim, p->weights != nullptr);
+    const bool many = many_rows(p->Sq * G);
+    const AttendLayout l = attend_layout(p->B, p->Hq, p->Sq, p->cache.dim, p->weights != nullptr, many);
     if (ws_bytes < l.bytes) return HQ_ERR_ARG;
     DeviceGuard dev(p->cache.k);
     if (!dev.ok) return HQ_ERR_ARG;
@@ -735,6 +600,6 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     a.lse2 = p->weights ? reinterpret_cast<float*>(base + l.lse2) : nullptr;
     a.ws = static_cast<WsHeader*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = p->cache.dim == 64 ? launch_attend<64>(a, st) : launch_attend<128>(a, st);
+    const cudaError_t e = p->cache.dim == 64 ? launch_attend<64>(a, many, st) : launch_attend<128>(a, many, st);
     return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }

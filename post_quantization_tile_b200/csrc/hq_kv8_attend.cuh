@@ -1,0 +1,210 @@
+// hq_kv8_attend.cuh -- what the two attention kernels over the e4m3 KV cache share: arguments, lengths
+// and masks, the division of the work into equal shares, and the join of the parts.
+#pragma once
+#include "hq_kv8.cuh"
+
+namespace hq {
+
+constexpr int kMaxBatch = 4096;   // sequences of one call (their prefix sums live in shared memory)
+constexpr float kBoost = 7.0f;    // probabilities are held times 2^7, and up to 2^8 times that
+constexpr float kSlack = 8.0f;    // before a larger maximum moves the reference they are relative to
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttendArgs {
+    hq_kv8_t c;
+    const __nv_bfloat16* q;
+    int64_t qb, qh, qs;
+    __nv_bfloat16* out;
+    int64_t ob, oh, os;
+    int B, Hq, Sq, G, page_shift;
+    const int32_t* table;
+    int64_t table_stride;
+    int64_t slots;  // max_pages * page
+    const int32_t* lens;
+    const int32_t* q_lens;
+    float scale;
+    int causal;
+    float* lse;
+    int64_t lb, lh;
+    const float* win;
+    float* w;
+    int64_t wib, wih, wb, wh, L;
+    uint32_t* prefix;  // [B + 1] share units before each sequence
+    float* part_o;     // [2 grid][rows of a unit][D]
+    float2* part_ml;   // [2 grid][rows of a unit]
+    float* lse2;       // [B][heads][G Sq] binary logarithm of the sums (weights only)
+    WsHeader* ws;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// lengths of sequence b: cached slots and queries, inside what the call's shapes allow
+struct SeqLen {
+    int n, m;
+    bool odd;
+};
+__device__ __forceinline__ SeqLen seq_len(const AttendArgs& a, int b)
+{
+    SeqLen s;
+    const int n = a.lens[b], m = a.q_lens ? a.q_lens[b] : a.Sq;
+    s.n = (int)max((int64_t)0, min((int64_t)n, a.slots));
+    s.m = max(0, min(m, a.Sq));
+    s.odd = n != s.n || m != s.m || (a.w && s.n > a.L);
+    return s;
+}
+// slots that query i of m sees, of n
+__device__ __forceinline__ int sees(const AttendArgs& a, int n, int m, int i)
+{
+    return a.causal ? max(0, n - m + i + 1) : n;
+}
+
+// first cache row (of [page][head][token]) of sixteen tokens from slot `tok`; -1 if their page is
+// outside the pool.  The entry points keep the number of rows below 2^31.
+__device__ __forceinline__ int locate(const AttendArgs& a, const int32_t* table, int h, int tok)
+{
+    const int32_t id = __ldg(table + (tok >> a.page_shift));
+    return id >= 0 && id < a.c.pages ? (int)(((uint32_t)id * a.c.heads + h) << a.page_shift) + (tok & (a.c.page - 1)) : -1;
+}
+
+// a finished row r of a unit: the output, the logarithm of its sum
+__device__ __forceinline__ void row_place(const AttendArgs& a, int h, int r, int& head, int& i)
+{
+    i = r / a.G;
+    head = h * a.G + (r - i * a.G);
+}
+__device__ __forceinline__ void write_lse(const AttendArgs& a, int b, int h, int r, float M, float l)
+{
+    int head, i;
+    row_place(a, h, r, head, i);
+    const float l2 = l > 0.0f ? M - kBoost + log2f(l) : (l == 0.0f ? -INFINITY : l);  // a NaN sum stays one
+    if (a.lse) a.lse[b * a.lb + head * a.lh + i] = l2 * kLn2;
+    if (a.lse2) a.lse2[((int64_t)b * a.c.heads + h) * a.G * a.Sq + r] = l2;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Shares.  A unit is U::R rows of one (sequence, key head) against their visible slots, in tiles of
+// U::TILE slots.  All units' tiles are laid end to end (sequences, then heads, then row tiles) and cut
+// into equal shares, one per thread block.
+// ------------------------------------------------------------------------------------------------
+// prefix sums of the sequences' tiles into `pre` [B + 1] (shared memory; block 0 also leaves them for the
+// join); `scan` holds one value per warp.  Returns whether this thread met a length out of range.
+template <class U, int THREADS>
+__device__ __forceinline__ bool share_prefix(const AttendArgs& a, uint32_t* pre, uint32_t* scan)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int run = (a.B + THREADS - 1) / THREADS, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
+    uint32_t mine = 0, last = 0;
+    bool odd = false;
+    for (int b = b0; b < b1; ++b) {
+        const SeqLen s = seq_len(a, b);
+        odd |= s.odd;
+        last = U::of_sequence(a, s);
+        mine += last;
+    }
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    uint32_t at = inc - mine;
+    for (int i = 0; i < warp; ++i) at += scan[i];
+    for (int b = b0; b < b1; ++b) {
+        pre[b] = at;
+        at += b1 - b0 == 1 ? last : U::of_sequence(a, seq_len(a, b));
+    }
+    if (tid == THREADS - 1) pre[a.B] = at;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= a.B; b += THREADS) a.prefix[b] = pre[b];
+    return odd;
+}
+
+// the part of a thread block's share [w0, w1) that lies in the unit of tile w0
+struct Segment {
+    int b, h, rt;
+    uint32_t t0, t1, tiles;  // tiles [t0, t1) of the unit's
+    SeqLen s;
+};
+template <class U>
+__device__ __forceinline__ Segment segment_at(const AttendArgs& a, const uint32_t* pre, uint32_t w0, uint32_t w1)
+{
+    Segment g;
+    g.b = 0;
+    for (int hi = a.B; hi - g.b > 1;) {
+        const int mid = (g.b + hi) >> 1;
+        if (pre[mid] <= w0) g.b = mid;
+        else hi = mid;
+    }
+    g.s = seq_len(a, g.b);
+    U::find(a, g.s, (pre[g.b + 1] - pre[g.b]) / a.c.heads, w0 - pre[g.b], g);
+    g.t1 = min(g.tiles, g.t0 + (w1 - w0));
+    return g;
+}
+
+// Joins the parts of the units that were cut, sixteen rows a thread block, and writes zeros where a row
+// sees nothing.  U: how the attention kernel makes units (U::R rows each) and lays them end to end.
+template <int D, class U>
+__global__ void __launch_bounds__(128) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
+{
+    const int r16 = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
+    const int h = bh % a.c.heads, b = bh / a.c.heads, rt = r16 / (U::R / 16), sub = r16 % (U::R / 16) * 16;
+    const SeqLen s = seq_len(a, b);
+    if (r16 * 16 >= s.m * a.G) return;
+    const uint32_t tiles = U::tiles(a, s, rt), W = a.prefix[a.B];
+    const uint32_t w0 = a.prefix[b] + U::before(a, s, h, rt), w1 = w0 + tiles;
+    // the share that holds share unit w: the smallest c with w < floor((c + 1) W / shares)
+    const uint32_t shares = min(W, (uint32_t)grid);
+    const int c0 = tiles ? (int)(((uint64_t)(w0 + 1) * shares - 1) / W) : 0;
+    const int c1 = tiles ? (int)(((uint64_t)w1 * shares - 1) / W) : 0;
+    if (tiles && c0 == c1) return;  // whole: written already
+    constexpr int TPR = 8, DPT = D / TPR;
+    const int r = sub + threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * DPT, rr = rt * U::R + r;
+    if (rr >= s.m * a.G) return;
+    float M = -INFINITY, L = 0.0f, y[DPT];
+#pragma unroll
+    for (int d = 0; d < DPT; ++d) y[d] = 0.0f;
+    if (tiles) {
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * c + (c == c0)) * U::R + r].x);
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t at = (int64_t)(2 * c + (c == c0)) * U::R + r;
+            const float2 ml = a.part_ml[at];
+            const float f = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
+            L = fmaf(ml.y, f, L);
+#pragma unroll
+            for (int d = 0; d < DPT; d += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + d0 + d);
+                y[d] = fmaf(x.x, f, y[d]), y[d + 1] = fmaf(x.y, f, y[d + 1]), y[d + 2] = fmaf(x.z, f, y[d + 2]), y[d + 3] = fmaf(x.w, f, y[d + 3]);
+            }
+        }
+    }
+    if (d0 == 0) write_lse(a, b, h, rr, M, L);
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    int head, i;
+    row_place(a, h, rr, head, i);
+    __nv_bfloat16* out = a.out + b * a.ob + head * a.oh + (int64_t)i * a.os + d0;
+#pragma unroll
+    for (int d = 0; d < DPT; d += 2) *reinterpret_cast<__nv_bfloat162*>(out + d) = __floats2bfloat162_rn(y[d] * inv, y[d + 1] * inv);
+}
+
+// what the attention entry point needs of the kernel for many rows (hq_kv8_prefill.cu)
+constexpr int kManyRows = 256;  // rows of its units
+cudaError_t launch_attend_many(const AttendArgs& a, int grid, cudaStream_t st);
+
+}  // namespace hq

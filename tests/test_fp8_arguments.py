@@ -135,9 +135,9 @@ def test_evict_refuses(L, bad, code):
 
 def test_workspace_sizes(L):
     assert L.hq_fp8_workspace_bytes() >= 64 + 8 * 4096
-    one = L.hq_kv8_attend_workspace_bytes(2, 8, 3, 128, 0)
-    assert one > L.hq_fp8_workspace_bytes() and L.hq_kv8_attend_workspace_bytes(2, 8, 3, 128, 1) >= one + 2 * 8 * 3 * 4
-    assert L.hq_kv8_attend_workspace_bytes(0, 8, 3, 128, 0) == 0 and L.hq_kv8_attend_workspace_bytes(2, 8, 3, 96, 0) == 0
+    one = L.hq_kv8_attend_workspace_bytes(2, 4, 8, 3, 128, 0)
+    assert one > L.hq_fp8_workspace_bytes() and L.hq_kv8_attend_workspace_bytes(2, 4, 8, 3, 128, 1) >= one + 2 * 8 * 3 * 4
+    assert L.hq_kv8_attend_workspace_bytes(0, 4, 8, 3, 128, 0) == 0 and L.hq_kv8_attend_workspace_bytes(2, 4, 8, 3, 96, 0) == 0
     assert L.hq_kv8_evict_workspace_bytes(2, 3, 10) >= 2 * 3 * 10 * 4 and L.hq_kv8_evict_workspace_bytes(2, 3, 0) == 0
 
 

@@ -75,7 +75,7 @@ def codes(hq, g, rows, cols, block):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("M,N,K_", [(1, 1, 1), (1, 128, 128), (7, 33, 200), (128, 128, 128), (129, 130, 131), (16, 1000, 48),
-                                    (300, 257, 1000), (1, 4096, 4096), (130, 5000, 640), (2000, 1300, 300), (2300, 2100, 300), (130, 19001, 200)])
+                                    (300, 257, 1000), (1, 4096, 4096), (130, 5000, 640), (2000, 1300, 300), (2300, 2100, 300), (2300, 2304, 200), (130, 19001, 200)])
 def test_gemm(hq, M, N, K_, dtype):
     g = torch.Generator().manual_seed(M + N + K_)
     a, w = codes(hq, g, M, K_, 1), codes(hq, g, N, K_, 128)

@@ -87,6 +87,57 @@ def test_attend_rows_of_a_group(hq, G, Sq, D):
     check_attend(hq, 2, 2, G, Sq, D, 16, [150, Sq], seed=G * 100 + Sq)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,Sq,lens,page", [(1, 128, [128], 64), (1, 129, [130], 16), (2, 128, [300], 128), (4, 70, [500, 70], 32),
+                                            (8, 40, [257, 1000, 40], 64), (3, 200, [200, 333], 16), (1, 17, [2000], 64),
+                                            (1, 300, [300], 64)])
+def test_attend_many_rows(hq, D, G, Sq, lens, page):
+    check_attend(hq, len(lens), 1, G, Sq, D, page, lens, seed=Sq + D, weights=False)
+
+
+def test_attend_many_rows_masks_and_ragged_queries(hq):
+    """No slots, fewer slots than queries, no queries, row tiles without rows, and all slots visible."""
+    for causal in (True, False):
+        check_attend(hq, 6, 2, 2, 150, 64, 32, [0, 30, 400, 64, 150, 257], q_lens=[150, 150, 70, 0, 150, 1], causal=causal, seed=50)
+    check_attend(hq, 2, 1, 5, 30, 128, 64, [90, 650], scale=-0.05, seed=51, strided=False)
+    check_attend(hq, 2, 1, 5, 30, 128, 64, [90, 65], scale=0.0, seed=52)
+    check_attend(hq, 3, 1, 4, 33, 64, 16, [0, 0, 0], seed=53, P=3)
+
+
+def test_attend_many_rows_stale_bytes_and_bad_pages(hq):
+    def stale(cache, k, v, table):
+        page = k.shape[2]
+        used = np.zeros(k.shape[:1] + k.shape[2:3], bool)
+        for b, n in enumerate([170, 116]):
+            for j in range(n):
+                used[table[b, j // page], j % page] = True
+        bad = torch.from_numpy(~used).cuda()[:, None, :, None].expand(*k.shape)
+        for t in (cache.k, cache.v):
+            t.view(torch.uint8).masked_fill_(bad, 0x7F)
+        return table
+    check_attend(hq, 2, 2, 3, 50, 128, 32, [170, 116], seed=54, change=stale, P=8)
+
+    def outside(cache, k, v, table):
+        table = table.copy()
+        table[0, 1], table[1, 0] = -1, 1 << 30
+        return table
+    check_attend(hq, 2, 1, 2, 100, 64, 16, [160, 140], seed=55, change=outside)
+
+
+def test_attend_many_rows_value_scales_far_apart(hq):
+    g = gen(56)
+    cache, (k, v, ks, vs), table = setup_cache(hq, g, 1, 5, 1, 64, 64)
+    for i, e in enumerate([0, -12, 6, -9, 3]):
+        cache.v_scale[int(table[0, i]), :] = 2.0 ** e
+        vs[int(table[0, i]), :] = 2.0 ** e
+        cache.k_scale[int(table[0, i]), :] *= 2.0 ** (i - 2)
+        ks[int(table[0, i]), :] *= 2.0 ** (i - 2)
+    q = torch.randn(1, 2, 40, 64, generator=g).to(torch.bfloat16).cuda()
+    out = hq.kv8_attend(q, cache, i32(table), i32([300]))
+    ref, rl, _, do, dl, _ = K.attend(K.values(q), k, v, ks, vs, table, [300], [40], 0.125, True)
+    assert np.all(np.abs(K.values(out) - ref) <= do + 2.0 ** -24 * np.abs(v).max() * vs.max())
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_attend_ragged_with_empty_rows(hq, causal):
     """No slots, fewer slots than queries (rows that see nothing), no queries, padded queries."""
