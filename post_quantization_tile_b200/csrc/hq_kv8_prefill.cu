@@ -24,7 +24,6 @@ namespace hq {
 namespace {
 
 constexpr int kThreadsP = 512;
-constexpr int kRegsSoftmax = 192, kRegsConvert = 80, kRegsIssue = 48;  // 4 x 128 at launch
 constexpr int kTok = 128;     // slots of a tile
 constexpr int kScaleRing = 4;  // tiles whose key scales are kept: the converter is at most two ahead
 
@@ -153,7 +152,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
 
     if (warp < 8) {
         // ---------------- softmax: row tile t, one row per thread ----------------
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lanes + 128 * t, to = lanes + 256 + 128 * t;
@@ -202,31 +200,33 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     wait(&sm.s_full[t], s_n + j);
                     if (!alive) continue;
                     tc_fence_after();
-                    uint32_t S[4][32];
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) tmem_ld32_nowait(ts + 32 * p, S[p]);
-                    const float4 ks0 = *reinterpret_cast<const float4*>(&sm.ks[(tile_n + j) % kScaleRing][0]);
-                    const float4 ks1 = *reinterpret_cast<const float4*>(&sm.ks[(tile_n + j) % kScaleRing][4]);
-                    const float ks[8] = {ks0.x, ks0.y, ks0.z, ks0.w, ks1.x, ks1.y, ks1.z, ks1.w};
-                    bool some_missing = false;
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) some_missing |= ks[y] < 0.0f;
-                    tmem_wait_ld();
-                    if (some_missing || tok + kTok > full_end) {
-#pragma unroll
-                        for (int p = 0; p < 4; ++p)
+                    // twice over the scores, 32 at a time with the next 32 on their way: keeping all 128 would
+                    // take the registers of a third warpgroup
+                    uint32_t S[2][32];
+                    tmem_ld32_nowait(ts, S[0]);
+                    const float* ks = sm.ks[(tile_n + j) % kScaleRing];
+                    const bool edge = tok + kTok > full_end || __any_sync(0xFFFFFFFFu, ks[lane & 7] < 0.0f);
+                    // slots that this row does not see, or whose page is missing
+                    auto hide = [&](uint32_t (&x)[32], int p, float k0, float k1) {
+                        if (edge)
 #pragma unroll
                             for (int y = 0; y < 32; ++y)
-                                if (tok + 32 * p + y >= end || ks[2 * p + (y >> 4)] < 0.0f) S[p][y] = 0xFF800000u;  // -infinity
-                    }
-                    float top = -INFINITY, cg[8];
+                                if (tok + 32 * p + y >= end || (y < 16 ? k0 : k1) < 0.0f) x[y] = 0xFF800000u;  // -infinity
+                    };
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int gq = 0; gq < 8; ++gq) {
-                        cg[gq] = c * fabsf(ks[gq]);
-                        float x = __uint_as_float(S[gq >> 1][(gq & 1) * 16]);
+                    for (int p = 0; p < 4; ++p) {
+                        tmem_wait_ld();
+                        tmem_ld32_nowait(ts + 32 * ((p + 1) & 3), S[(p + 1) & 1]);
+                        const float k0 = ks[2 * p], k1 = ks[2 * p + 1];
+                        hide(S[p & 1], p, k0, k1);
+                        float x0 = __uint_as_float(S[p & 1][0]), x1 = __uint_as_float(S[p & 1][16]);
 #pragma unroll
-                        for (int y = 1; y < 16; ++y) x = fmaxf(x, __uint_as_float(S[gq >> 1][(gq & 1) * 16 + y]));
-                        top = fmaxf(top, x * cg[gq]);
+                        for (int y = 1; y < 16; ++y) {
+                            x0 = fmaxf(x0, __uint_as_float(S[p & 1][y]));
+                            x1 = fmaxf(x1, __uint_as_float(S[p & 1][16 + y]));
+                        }
+                        top = fmaxf(top, fmaxf(x0 * (c * fabsf(k0)), x1 * (c * fabsf(k1))));
                     }
                     const bool moves = top > m + kSlack;
                     if (__any_sync(0xFFFFFFFFu, moves)) {
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                         l *= f;
                         m = next;
                         if (j > 0) {  // the accumulator's products so far are done: this tile's scores came after them
-#pragma unroll
+#pragma unroll 1
                             for (int p = 0; p < D / 32; ++p) {
                                 uint32_t o[32];
                                 tmem_ld32_nowait(to + 32 * p, o);
@@ -249,20 +249,24 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     const float2 nsub = make_float2(-sub, -sub);
                     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t P[32];
+                    for (int p = 0; p < 4; ++p) {
+                        tmem_wait_ld();
+                        if (p < 3) tmem_ld32_nowait(ts + 32 * (p + 1), S[(p + 1) & 1]);
+                        const float k0 = ks[2 * p], k1 = ks[2 * p + 1];
+                        hide(S[p & 1], p, k0, k1);
+                        const float c0 = c * fabsf(k0), c1 = c * fabsf(k1);
+                        uint32_t P[16];
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            const int e0 = 2 * y, q4 = 2 * p + (e0 >> 5);
-                            const float cq = cg[4 * p + (e0 >> 4)];
-                            float2 x = __ffma2_rn(make_float2(__uint_as_float(S[q4][e0 & 31]), __uint_as_float(S[q4][(e0 & 31) + 1])),
+                        for (int y = 0; y < 16; ++y) {
+                            const float cq = y < 8 ? c0 : c1;
+                            float2 x = __ffma2_rn(make_float2(__uint_as_float(S[p & 1][2 * y]), __uint_as_float(S[p & 1][2 * y + 1])),
                                                   make_float2(cq, cq), nsub);
                             x.x = ex2(x.x);
                             x.y = ex2(x.y);
                             sum = f2add(sum, x);
                             P[y] = pack_f16(x.x, x.y);
                         }
-                        tmem_st32(ts + 32 * p, P);
+                        tmem_st16(ts + 16 * p, P);
                     }
                     l += sum.x + sum.y;
                     tmem_wait_st();
@@ -323,7 +327,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
         }
     } else if (warp < 12) {
         // ---------------- conversion: codes from the cache to binary16 operand tiles ----------------
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConvert));
         constexpr int CPR = D / 16, RPP = 128 / CPR, PASSES = 128 / RPP;  // chunks of a row, rows of a pass
         const int ct = tid - 256, c = ct % CPR, row0 = ct / CPR;
         uint32_t seg_n = 0, tile_n = 0;
@@ -344,44 +347,52 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
             named_sync(1, 128);
             vmax = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
             const float vref = vmax > 0.0f ? vmax : 1.0f;
-#pragma unroll 1
-            for (int j = 0; j < T; ++j, ++tile_n) {
-                const int st = tile_n & 1, tok = (int)(g.t0 + j) * kTok;
-                // the cache rows of this thread's operand rows; a group of sixteen lies in one page
-                int at[PASSES];
-                uint4 x[PASSES];
+            // the groups of sixteen slots of a tile: lane y < 8 knows the first cache row and the scales of
+            // group y, one tile ahead of the codes; the keys of the next tile and the values of this one are
+            // on their way while the tile before is stored
+            int g_row = -1;
+            float2 g_scale = make_float2(-1.0f, 0.0f);
+            auto find_groups = [&](int j) {
+                const int tok = (int)(g.t0 + j) * kTok + 16 * (lane & 7);
+                g_row = j < T && tok < end ? locate(a, table, g.h, tok) : -1;
+                g_scale = j < T && tok < end ? make_float2(-1.0f, 0.0f) : make_float2(1.0f, 0.0f);
+                if (g_row >= 0) {
+                    const int ph = g_row >> a.page_shift;
+                    g_scale = make_float2(__ldg(a.c.k_scale + ph), __ldg(a.c.v_scale + ph));
+                }
+            };
+            auto fetch = [&](uint4 (&x)[PASSES], const uint8_t* codes, int j) {
 #pragma unroll
                 for (int p = 0; p < PASSES; ++p) {
-                    const int tk = tok + p * RPP + row0;
-                    at[p] = tk < end ? locate(a, table, g.h, tk & ~15) : -1;
-                    if (at[p] >= 0) at[p] += tk & 15;
+                    const int tk = p * RPP + row0, row = __shfl_sync(0xFFFFFFFFu, g_row, tk >> 4);
+                    x[p] = row >= 0 && (int)(g.t0 + j) * kTok + tk < end
+                               ? __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)(row + (tk & 15)) * D) + c)
+                               : make_uint4(0u, 0u, 0u, 0u);
                 }
-#pragma unroll
-                for (int p = 0; p < PASSES; ++p)
-                    x[p] = at[p] >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.c.k + (int64_t)at[p] * D) + c) : make_uint4(0u, 0u, 0u, 0u);
-                float ks = -1.0f;
-                if (ct < 8 && tok + 16 * ct < end) {
-                    const int row = locate(a, table, g.h, tok + 16 * ct);
-                    if (row >= 0) ks = __ldg(a.c.k_scale + (row >> a.page_shift));
-                }
+            };
+            uint4 xk[PASSES], xv[PASSES];
+            find_groups(0);
+            fetch(xk, a.c.k, 0);
+#pragma unroll 1
+            for (int j = 0; j < T; ++j, ++tile_n) {
+                const int st = tile_n & 1;
+                fetch(xv, a.c.v, j);
+                const float ks = g_scale.x, vr = g_scale.y / vref;
+                const uint32_t vr2 = pack_f16(vr, vr);
+                find_groups(j + 1);
                 if (tile_n >= 2) wait(&sm.k_empty[st], tile_n / 2 - 1);
-                if (ct < 8) sm.ks[tile_n % kScaleRing][ct] = tok + 16 * ct < end ? ks : 1.0f;
+                if (ct < 8) sm.ks[tile_n % kScaleRing][ct] = ks;
                 if (ct == 0 && j == 0) sm.vref[seg_n & 3] = vref;
 #pragma unroll
-                for (int p = 0; p < PASSES; ++p) put_codes<D, false>(sm.k[st], p * RPP + row0, c, x[p], 0u);
+                for (int p = 0; p < PASSES; ++p) put_codes<D, false>(sm.k[st], p * RPP + row0, c, xk[p], 0u);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.k_full[st]);
-                uint32_t ratio[PASSES];
-#pragma unroll
-                for (int p = 0; p < PASSES; ++p) {
-                    x[p] = at[p] >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.c.v + (int64_t)at[p] * D) + c) : make_uint4(0u, 0u, 0u, 0u);
-                    const float vr = at[p] >= 0 ? __ldg(a.c.v_scale + (at[p] >> a.page_shift)) / vref : 0.0f;
-                    ratio[p] = pack_f16(vr, vr);
-                }
+                if (j + 1 < T) fetch(xk, a.c.k, j + 1);
                 if (tile_n >= 2) wait(&sm.v_empty[st], tile_n / 2 - 1);
 #pragma unroll
-                for (int p = 0; p < PASSES; ++p) put_codes<D, true>(sm.v[st], p * RPP + row0, c, x[p], ratio[p]);
+                for (int p = 0; p < PASSES; ++p)
+                    put_codes<D, true>(sm.v[st], p * RPP + row0, c, xv[p], __shfl_sync(0xFFFFFFFFu, vr2, (p * RPP + row0) >> 4));
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.v_full[st]);
@@ -390,7 +401,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
             w0 += T;
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (warp == 12) {
             // ---------------- MMA issue (one lane; the whole warp walks along for the waits) ----------------
             constexpr uint32_t IDS = idesc_f16(128, 128, false), IDO = idesc_f16(128, D, true);
