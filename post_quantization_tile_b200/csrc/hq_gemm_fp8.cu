@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
     using C = F8Cfg<GN>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     F8Smem<GN>& sm = *reinterpret_cast<F8Smem<GN>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int KB = (int)((a.K + GK - 1) / GK);
     const int NT = (int)((a.N + GN - 1) / GN);
     const int64_t tiles = ((a.M + GM - 1) / GM) * NT;
@@ -152,30 +152,29 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0;
-            bool alive = true;
-            for (int64_t tile = blockIdx.x; alive && tile < tiles; tile += gridDim.x) {
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % C::STAGES, slot = it % C::ACC;
-                    if ((it >= C::ACC && !mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / C::ACC - 1) & 1))) ||
-                        !mbar_wait_sleep(&sm.full[s], (uint32_t)((it / C::STAGES) & 1))) {
-                        atomicOr(&sm.status, kStTimeout);
-                        alive = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = sw128_desc(sm.a[s]), bd = sw128_desc(sm.b[s]);
-#pragma unroll
-                    for (int kk = 0; kk < GK / 32; ++kk)  // K 32 per MMA: the start address moves 32 bytes
-                        mma_f8(tbase + (uint32_t)(slot * GN), ad + (uint64_t)(2 * kk), bd + (uint64_t)(2 * kk), C::IDESC,
-                               kk > 0 ? 1u : 0u);
-                    mma_commit(&sm.empty[s]);
-                    mma_commit(&sm.acc_full[slot]);
+        const uint64_t ad0 = sw128_desc(sm.a[0]), bd0 = sw128_desc(sm.b[0]);
+        const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+        int it = 0;
+        bool alive = true;
+        for (int64_t tile = blockIdx.x; alive && tile < tiles; tile += gridDim.x) {
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int s = it % C::STAGES, slot = it % C::ACC;
+                const bool got = (it < C::ACC || mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / C::ACC - 1) & 1))) &&
+                                 mbar_wait_sleep(&sm.full[s], (uint32_t)((it / C::STAGES) & 1));
+                if (!__all_sync(0xFFFFFFFFu, got)) {
+                    if (lane == 0) atomicOr(&sm.status, kStTimeout);
+                    alive = false;
+                    break;
                 }
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < GK / 32; ++kk)  // K 32 per MMA: the start address moves 32 bytes
+                    mma_f8(tb + (uint32_t)(slot * GN), ad0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk),
+                           bd0 + (uint64_t)(s * (GN * GK / 16) + 2 * kk), C::IDESC, kk > 0 ? 1u : 0u);
+                mma_commit_warp(&sm.empty[s]);
+                mma_commit_warp(&sm.acc_full[slot]);
             }
         }
-        __syncwarp();
     } else {
         // warpgroup h takes columns 32 h .. 32 h + 31 of each slot; a warp reads the TMEM lane quarter
         // warp % 4, one row of the tile per thread
@@ -255,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     PairSmem& sm = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int KB = (int)((a.K + GK - 1) / GK);
     const int NT = (int)((a.N + PN - 1) / PN);
@@ -305,24 +304,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
             if (rank == 0)
                 for (int j = it > PSTAGES ? it - PSTAGES : 0; j < it; ++j)
                     mbar_wait_sleep(&sm.full[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
+            const uint64_t ad0 = sw128_desc(sm.a[0]), bd0 = sw128_desc(sm.b[0]);
+            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
             int it = 0;
             bool alive = true;
             for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % PSTAGES, slot = it % PACC;
-                    if ((it >= PACC && !mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / PACC - 1) & 1))) ||
-                        !mbar_wait_sleep(&sm.full[s], (uint32_t)((it / PSTAGES) & 1))) {
-                        atomicOr(&sm.status, kStTimeout);
+                    const bool got = (it < PACC || mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / PACC - 1) & 1))) &&
+                                     mbar_wait_sleep(&sm.full[s], (uint32_t)((it / PSTAGES) & 1));
+                    if (!__all_sync(0xFFFFFFFFu, got)) {
+                        if (lane == 0) atomicOr(&sm.status, kStTimeout);
                         alive = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = sw128_desc(sm.a[s]), bd = sw128_desc(sm.b[s]);
 #pragma unroll
                     for (int kk = 0; kk < GK / 32; ++kk)
-                        mma_f8_pair(tbase + (uint32_t)(slot * PN), ad + (uint64_t)(2 * kk), bd + (uint64_t)(2 * kk),
-                                    idesc_f8(2 * GM, PN), kk > 0 ? 1u : 0u);
+                        mma_f8_pair(tb + (uint32_t)(slot * PN), ad0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk),
+                                    bd0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk), idesc_f8(2 * GM, PN), kk > 0 ? 1u : 0u);
                     mma_commit_pair(&sm.empty[s]);
                     mma_commit_pair(&sm.acc_full[slot]);
                 }

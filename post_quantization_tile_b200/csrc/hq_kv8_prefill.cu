@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kThreadsP = 512;
 constexpr int kTok = 128;     // slots of a tile
+constexpr int kPoly = 1, kPolyOf = 2;  // pairs of exponentials on the multiply-add pipe, of so many
 constexpr int kScaleRing = 4;  // tiles whose key scales are kept: the converter is at most two ahead
 
 // units of 256 rows; a unit's tiles end with the last slot that any of its rows sees
@@ -81,9 +82,10 @@ struct PrefillSmem {
     uint32_t scan[kThreadsP / 32];
 };
 
-// sixteen codes of one row (16-byte chunk c of it) as binary16, times r, into a swizzled operand tile
-template <int D, bool SCALE>
-__device__ __forceinline__ void put_codes(unsigned char (*tile)[PrefillSmem<D>::HALF], int row, int c, uint4 x, uint32_t r2)
+// sixteen codes of a row (16-byte chunk c of 64) as binary16, times r2, into a swizzled operand run.  The
+// lanes of a store are eight rows by four chunks, which meet in no bank.
+template <bool SCALE>
+__device__ __forceinline__ void put_codes(unsigned char* run, int row, int c, uint4 x, uint32_t r2)
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t h[8];
@@ -98,14 +100,26 @@ __device__ __forceinline__ void put_codes(unsigned char (*tile)[PrefillSmem<D>::
             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), *reinterpret_cast<const __half2*>(&r2));
             h[i] = *reinterpret_cast<const uint32_t*>(&y);
         }
-    // chunks 4 .. 7 go to the second run, whose banks are the first one's: those lanes store their second
-    // half first, so that eight lanes of a row meet in no bank
-    unsigned char* to = tile[c >> 2];
-    const int cc = (c & 3) * 2;
-    const bool odd = c >= 4;
-    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-    *reinterpret_cast<uint4*>(to + swz(row, cc + odd)) = odd ? hi : lo;
-    *reinterpret_cast<uint4*>(to + swz(row, cc + !odd)) = odd ? lo : hi;
+    *reinterpret_cast<uint4*>(run + swz(row, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(run + swz(row, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// 2^x of a pair on the multiply-add pipe (the exponential unit gives 16 results a cycle and would bound
+// the softmax): x = n + f with n the nearest integer, 2^f by its degree-4 minimax polynomial on
+// [-1/2, 1/2] (relative error 2.6e-6), n added to the exponent.  x up to 126; below -126: 2^-126.
+__device__ __forceinline__ float2 exp2_poly(float2 x)
+{
+    const float magic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are n, the rest vanishes in the shift below
+    x.x = fmaxf(x.x, -126.0f);
+    x.y = fmaxf(x.y, -126.0f);
+    const float2 t = f2add(x, make_float2(magic, magic));
+    const float2 f = f2sub(x, f2sub(t, make_float2(magic, magic)));
+    float2 p = __ffma2_rn(f, make_float2(0.00957010128f, 0.00957010128f), make_float2(0.0559178591f, 0.0559178591f));
+    p = __ffma2_rn(p, f, make_float2(0.240247443f, 0.240247443f));
+    p = __ffma2_rn(p, f, make_float2(0.693121791f, 0.693121791f));
+    p = __ffma2_rn(p, f, make_float2(0.999999285f, 0.999999285f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
 template <int D>
@@ -115,7 +129,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
     using Smem = PrefillSmem<D>;
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint32_t* pre = reinterpret_cast<uint32_t*>(&sm + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.k_full[i], 4);
@@ -200,32 +214,42 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     wait(&sm.s_full[t], s_n + j);
                     if (!alive) continue;
                     tc_fence_after();
+                    const float* ks = sm.ks[(tile_n + j) % kScaleRing];
+                    if (tok + kTok > full_end || __any_sync(0xFFFFFFFFu, ks[lane & 7] < 0.0f)) {
+                        // a tile with slots that some row does not see, or whose page is missing: their scores
+                        // become -infinity where they lie, so that the passes below know no masks
+#pragma unroll 1
+                        for (int p = 0; p < 4; ++p) {
+                            uint32_t x[32];
+                            tmem_ld32_nowait(ts + 32 * p, x);
+                            tmem_wait_ld();
+                            const bool no0 = ks[2 * p] < 0.0f, no1 = ks[2 * p + 1] < 0.0f;
+                            const int left = end - tok - 32 * p;
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                if (y >= left || (y < 16 ? no0 : no1)) x[y] = 0xFF800000u;
+                            tmem_st32(ts + 32 * p, x);
+                        }
+                        tmem_wait_st();
+                    }
                     // twice over the scores, 32 at a time with the next 32 on their way: keeping all 128 would
                     // take the registers of a third warpgroup
                     uint32_t S[2][32];
                     tmem_ld32_nowait(ts, S[0]);
-                    const float* ks = sm.ks[(tile_n + j) % kScaleRing];
-                    const bool edge = tok + kTok > full_end || __any_sync(0xFFFFFFFFu, ks[lane & 7] < 0.0f);
-                    // slots that this row does not see, or whose page is missing
-                    auto hide = [&](uint32_t (&x)[32], int p, float k0, float k1) {
-                        if (edge)
-#pragma unroll
-                            for (int y = 0; y < 32; ++y)
-                                if (tok + 32 * p + y >= end || (y < 16 ? k0 : k1) < 0.0f) x[y] = 0xFF800000u;  // -infinity
-                    };
                     float top = -INFINITY;
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
                         tmem_wait_ld();
                         tmem_ld32_nowait(ts + 32 * ((p + 1) & 3), S[(p + 1) & 1]);
                         const float k0 = ks[2 * p], k1 = ks[2 * p + 1];
-                        hide(S[p & 1], p, k0, k1);
-                        float x0 = __uint_as_float(S[p & 1][0]), x1 = __uint_as_float(S[p & 1][16]);
+                        float x[8];
 #pragma unroll
-                        for (int y = 1; y < 16; ++y) {
-                            x0 = fmaxf(x0, __uint_as_float(S[p & 1][y]));
-                            x1 = fmaxf(x1, __uint_as_float(S[p & 1][16 + y]));
-                        }
+                        for (int z = 0; z < 8; ++z) x[z] = __uint_as_float(S[p & 1][4 * z]);
+#pragma unroll
+                        for (int y = 1; y < 4; ++y)
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) x[z] = fmaxf(x[z], __uint_as_float(S[p & 1][4 * z + y]));
+                        const float x0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), x1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
                         top = fmaxf(top, fmaxf(x0 * (c * fabsf(k0)), x1 * (c * fabsf(k1))));
                     }
                     const bool moves = top > m + kSlack;
@@ -253,7 +277,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                         tmem_wait_ld();
                         if (p < 3) tmem_ld32_nowait(ts + 32 * (p + 1), S[(p + 1) & 1]);
                         const float k0 = ks[2 * p], k1 = ks[2 * p + 1];
-                        hide(S[p & 1], p, k0, k1);
                         const float c0 = c * fabsf(k0), c1 = c * fabsf(k1);
                         uint32_t P[16];
 #pragma unroll
@@ -261,8 +284,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                             const float cq = y < 8 ? c0 : c1;
                             float2 x = __ffma2_rn(make_float2(__uint_as_float(S[p & 1][2 * y]), __uint_as_float(S[p & 1][2 * y + 1])),
                                                   make_float2(cq, cq), nsub);
-                            x.x = ex2(x.x);
-                            x.y = ex2(x.y);
+                            if (y % kPolyOf < kPoly) x = exp2_poly(x);
+                            else x = make_float2(ex2(x.x), ex2(x.y));
                             sum = f2add(sum, x);
                             P[y] = pack_f16(x.x, x.y);
                         }
@@ -274,6 +297,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_ready[t]);
                 }
+                if (m == -INFINITY) l = 0.0f;  // no slot seen: not even the polynomial's smallest value
                 // the segment's accumulator
                 wait(&sm.o_full[t], seg_n);
                 if (alive) {
@@ -327,8 +351,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
         }
     } else if (warp < 12) {
         // ---------------- conversion: codes from the cache to binary16 operand tiles ----------------
-        constexpr int CPR = D / 16, RPP = 128 / CPR, PASSES = 128 / RPP;  // chunks of a row, rows of a pass
-        const int ct = tid - 256, c = ct % CPR, row0 = ct / CPR;
+        // a pass: 32 rows by 64 dims; a warp's eight rows lie in one group of sixteen slots
+        constexpr int RUNS = D / 64, PASSES = 4 * RUNS;
+        const int ct = tid - 256, c = ct & 3, row0 = ct >> 2, half = ct >> 6;
         uint32_t seg_n = 0, tile_n = 0;
         while (w0 < w1) {
             const Segment g = segment_at<ManyRows>(a, pre, w0, w1);
@@ -347,52 +372,68 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
             named_sync(1, 128);
             vmax = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
             const float vref = vmax > 0.0f ? vmax : 1.0f;
-            // the groups of sixteen slots of a tile: lane y < 8 knows the first cache row and the scales of
-            // group y, one tile ahead of the codes; the keys of the next tile and the values of this one are
-            // on their way while the tile before is stored
-            int g_row = -1;
+            // the groups of sixteen slots of a tile: lane y < 8 knows the page (two tiles ahead of the codes),
+            // the first cache row and the scales (one ahead) of group y; the keys of the next tile and the
+            // values of this one are on their way while the tile before is stored
+            const int gy = lane & 7, stop = T * kTok;
+            int g_id = -1, g_row = -1;
             float2 g_scale = make_float2(-1.0f, 0.0f);
-            auto find_groups = [&](int j) {
-                const int tok = (int)(g.t0 + j) * kTok + 16 * (lane & 7);
-                g_row = j < T && tok < end ? locate(a, table, g.h, tok) : -1;
-                g_scale = j < T && tok < end ? make_float2(-1.0f, 0.0f) : make_float2(1.0f, 0.0f);
-                if (g_row >= 0) {
-                    const int ph = g_row >> a.page_shift;
-                    g_scale = make_float2(__ldg(a.c.k_scale + ph), __ldg(a.c.v_scale + ph));
-                }
+            const int tok0 = (int)g.t0 * kTok;
+            auto find_pages = [&](int j) {
+                const int at = j * kTok + 16 * gy;
+                g_id = at < stop && tok0 + at < end ? __ldg(table + ((tok0 + at) >> a.page_shift)) : -2;
             };
-            auto fetch = [&](uint4 (&x)[PASSES], const uint8_t* codes, int j) {
+            auto find_rows = [&](int j) {
+                const bool ok = g_id >= 0 && g_id < a.c.pages;
+                const int ph = ok ? g_id * a.c.heads + g.h : 0;
+                g_row = ok ? (ph << a.page_shift) + ((tok0 + j * kTok + 16 * gy) & (a.c.page - 1)) : -1;
+                // -2, behind the segment's last slot: hidden by the rows' ends, any positive key scale will do
+                g_scale = ok ? make_float2(__ldg(a.c.k_scale + ph), __ldg(a.c.v_scale + ph)) : make_float2(g_id == -2 ? 1.0f : -1.0f, 0.0f);
+            };
+            // rows of a missing group come from the pool's first page; the values are cleared below
+            auto fetch = [&](uint4 (&x)[PASSES], const uint8_t* codes) {
 #pragma unroll
                 for (int p = 0; p < PASSES; ++p) {
-                    const int tk = p * RPP + row0, row = __shfl_sync(0xFFFFFFFFu, g_row, tk >> 4);
-                    x[p] = row >= 0 && (int)(g.t0 + j) * kTok + tk < end
-                               ? __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)(row + (tk & 15)) * D) + c)
-                               : make_uint4(0u, 0u, 0u, 0u);
+                    const int row = __shfl_sync(0xFFFFFFFFu, g_row, 2 * (p / RUNS) + half);
+                    x[p] = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)(max(row, 0) + (row0 & 15)) * D + (p % RUNS) * 64) + c);
                 }
             };
             uint4 xk[PASSES], xv[PASSES];
-            find_groups(0);
-            fetch(xk, a.c.k, 0);
+            find_pages(0);
+            find_rows(0);
+            find_pages(1);
+            fetch(xk, a.c.k);
 #pragma unroll 1
             for (int j = 0; j < T; ++j, ++tile_n) {
                 const int st = tile_n & 1;
-                fetch(xv, a.c.v, j);
+                fetch(xv, a.c.v);
                 const float ks = g_scale.x, vr = g_scale.y / vref;
                 const uint32_t vr2 = pack_f16(vr, vr);
-                find_groups(j + 1);
+                // values that nobody may see are zeros: behind the last slot, and of missing pages
+                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, g_row < 0) & 0xFFu;
+                const bool edge = gone != 0u || tok0 + (j + 1) * kTok > end;
+                find_rows(j + 1);
+                find_pages(j + 2);
                 if (tile_n >= 2) wait(&sm.k_empty[st], tile_n / 2 - 1);
                 if (ct < 8) sm.ks[tile_n % kScaleRing][ct] = ks;
                 if (ct == 0 && j == 0) sm.vref[seg_n & 3] = vref;
 #pragma unroll
-                for (int p = 0; p < PASSES; ++p) put_codes<D, false>(sm.k[st], p * RPP + row0, c, xk[p], 0u);
+                for (int p = 0; p < PASSES; ++p) put_codes<false>(sm.k[st][p % RUNS], (p / RUNS) * 32 + row0, c, xk[p], 0u);
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.k_full[st]);
-                if (j + 1 < T) fetch(xk, a.c.k, j + 1);
+                fetch(xk, a.c.k);
                 if (tile_n >= 2) wait(&sm.v_empty[st], tile_n / 2 - 1);
+                if (edge)
+#pragma unroll
+                    for (int p = 0; p < PASSES; ++p) {
+                        const int r = (p / RUNS) * 32 + row0;
+                        if ((gone >> (r >> 4) & 1u) || tok0 + j * kTok + r >= end) xv[p] = make_uint4(0u, 0u, 0u, 0u);
+                    }
 #pragma unroll
                 for (int p = 0; p < PASSES; ++p)
-                    put_codes<D, true>(sm.v[st], p * RPP + row0, c, xv[p], __shfl_sync(0xFFFFFFFFu, vr2, (p * RPP + row0) >> 4));
+                    put_codes<true>(sm.v[st][p % RUNS], (p / RUNS) * 32 + row0, c, xv[p],
+                                    __shfl_sync(0xFFFFFFFFu, vr2, 2 * (p / RUNS) + half));
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.v_full[st]);
@@ -402,33 +443,31 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
         }
     } else {
         if (warp == 12) {
-            // ---------------- MMA issue (one lane; the whole warp walks along for the waits) ----------------
+            // ---------------- MMA issue ----------------
             constexpr uint32_t IDS = idesc_f16(128, 128, false), IDO = idesc_f16(128, D, true);
             uint32_t seg_n = 0, tile_n = 0, s_n[2] = {0, 0};
+            // operand tiles follow one another: descriptors differ by their distance in 16-byte units
+            constexpr uint64_t RUN = Smem::HALF >> 4, TILE = (D / 64) * RUN;
+            const uint64_t dq = sw128_desc(sm.q[0][0]), dk = sw128_desc(sm.k[0][0]), dv = sw128_desc_mn(sm.v[0][0], Smem::HALF);
+            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
             auto score = [&](int t, int st) {
-                if (lane == 0) {
+                const uint64_t ad = dq + (t ? TILE : 0), bd = dk + (st ? TILE : 0);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t ad = sw128_desc(sm.q[t][kk >> 2]) + (uint64_t)(2 * (kk & 3));
-                        const uint64_t bd = sw128_desc(sm.k[st][kk >> 2]) + (uint64_t)(2 * (kk & 3));
-                        mma_f16_ss(tbase + 128 * t, ad, bd, IDS, kk > 0);
-                    }
-                    mma_commit(&sm.s_full[t]);
-                }
-                __syncwarp();
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_f16_ss(tb + 128 * t, ad + (kk >> 2) * RUN + 2 * (kk & 3), bd + (kk >> 2) * RUN + 2 * (kk & 3), IDS, kk > 0);
+                mma_commit_warp(&sm.s_full[t]);
             };
             while (w0 < w1) {
                 const Segment g = segment_at<ManyRows>(a, pre, w0, w1);
-                const int T = (int)(g.t1 - g.t0);
-                const int nt = g.rt * kManyRows + 128 < g.s.m * a.G ? 2 : 1;  // row tiles with rows
+                const int T = __shfl_sync(0xFFFFFFFFu, (int)(g.t1 - g.t0), 0);
+                const int nt = __shfl_sync(0xFFFFFFFFu, g.rt * kManyRows + 128 < g.s.m * a.G ? 2 : 1, 0);  // row tiles with rows
                 wait(&sm.q_ready[0], seg_n);
                 wait(&sm.q_ready[1], seg_n);
                 wait(&sm.k_full[tile_n & 1], tile_n / 2);
                 tc_fence_after();
                 if (alive) {
                     for (int t = 0; t < nt; ++t) score(t, tile_n & 1);
-                    if (lane == 0) mma_commit(&sm.k_empty[tile_n & 1]);
-                    __syncwarp();
+                    mma_commit_warp(&sm.k_empty[tile_n & 1]);
                 }
 #pragma unroll 1
                 for (int j = 0; j < T; ++j, ++tile_n) {
@@ -439,20 +478,17 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                         if (t == 0 && j + 1 < T) wait(&sm.k_full[next], (tile_n + 1) / 2);
                         tc_fence_after();
                         if (!alive) continue;
-                        if (lane == 0) {
 #pragma unroll
-                            for (int kk = 0; kk < kTok / 16; ++kk)
-                                mma_f16_ts(tbase + 256 + 128 * t, tbase + 128 * t + 8 * kk,
-                                           sw128_desc_mn(sm.v[st][0], Smem::HALF) + (uint64_t)(128 * kk), IDO, j > 0 || kk > 0);
-                            if (t == nt - 1) mma_commit(&sm.v_empty[st]);
-                            if (j + 1 == T) mma_commit(&sm.o_full[t]);
-                            if (j + 1 == T && nt == 1) mma_commit(&sm.o_full[1]);
-                        }
-                        __syncwarp();
+                        for (int kk = 0; kk < kTok / 16; ++kk)
+                            mma_f16_ts(tb + 256 + 128 * t, tb + 128 * t + 8 * kk, dv + (st ? TILE : 0) + (uint64_t)(128 * kk), IDO,
+                                       j > 0 || kk > 0);
+                        if (t == nt - 1) mma_commit_warp(&sm.v_empty[st]);
                         if (j + 1 < T) {
                             score(t, next);
-                            if (t == nt - 1 && lane == 0) mma_commit(&sm.k_empty[next]);
-                            __syncwarp();
+                            if (t == nt - 1) mma_commit_warp(&sm.k_empty[next]);
+                        } else {
+                            mma_commit_warp(&sm.o_full[t]);
+                            if (nt == 1) mma_commit_warp(&sm.o_full[1]);
                         }
                     }
                 }
@@ -460,10 +496,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                 w0 += T;
             }
             // nothing may be under way when the tensor memory is given back
-            if (lane == 0) {
-                mma_commit(&sm.drain);
-                mbar_wait_sleep(&sm.drain, 0);
-            }
+            mma_commit_warp(&sm.drain);
+            mbar_wait_sleep(&sm.drain, 0);
             __syncwarp();
         }
     }
