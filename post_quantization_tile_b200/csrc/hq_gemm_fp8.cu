@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         const uint64_t ad0 = sw128_desc(sm.a[0]), bd0 = sw128_desc(sm.b[0]);
-        const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+        const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), leader = elect_lane();
         int it = 0;
         bool alive = true;
         for (int64_t tile = blockIdx.x; alive && tile < tiles; tile += gridDim.x) {
@@ -170,9 +170,9 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
 #pragma unroll
                 for (int kk = 0; kk < GK / 32; ++kk)  // K 32 per MMA: the start address moves 32 bytes
                     mma_f8(tb + (uint32_t)(slot * GN), ad0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk),
-                           bd0 + (uint64_t)(s * (GN * GK / 16) + 2 * kk), C::IDESC, kk > 0 ? 1u : 0u);
-                mma_commit_warp(&sm.empty[s]);
-                mma_commit_warp(&sm.acc_full[slot]);
+                           bd0 + (uint64_t)(s * (GN * GK / 16) + 2 * kk), C::IDESC, kk > 0 ? 1u : 0u, leader);
+                mma_commit_warp(&sm.empty[s], leader);
+                mma_commit_warp(&sm.acc_full[slot], leader);
             }
         }
     } else {
@@ -306,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
                     mbar_wait_sleep(&sm.full[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
         } else if (warp == 1 && rank == 0) {
             const uint64_t ad0 = sw128_desc(sm.a[0]), bd0 = sw128_desc(sm.b[0]);
-            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
+            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), leader = elect_lane();
             int it = 0;
             bool alive = true;
             for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
@@ -323,9 +323,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
 #pragma unroll
                     for (int kk = 0; kk < GK / 32; ++kk)
                         mma_f8_pair(tb + (uint32_t)(slot * PN), ad0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk),
-                                    bd0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk), idesc_f8(2 * GM, PN), kk > 0 ? 1u : 0u);
-                    mma_commit_pair(&sm.empty[s]);
-                    mma_commit_pair(&sm.acc_full[slot]);
+                                    bd0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk), idesc_f8(2 * GM, PN), kk > 0 ? 1u : 0u, leader);
+                    mma_commit_pair(&sm.empty[s], leader);
+                    mma_commit_pair(&sm.acc_full[slot], leader);
                 }
             }
         }

@@ -1,15 +1,14 @@
 // hq_kv8_prefill.cu -- attention of many query rows over the e4m3 KV cache (prompt chunks, long
 // speculative runs): both products on tcgen05 with TMEM accumulators.
 //
-// A unit is 256 rows of one (sequence, key head), two tiles of 128, against tiles of 128 slots.  Per slot
-// tile and row tile: S = Q K^T (eight MMAs M 128, N 128, K 16) into TMEM, softmax by 128 threads with
-// one row each, P as binary16 back into the same TMEM columns, O += P V (P from TMEM).  The two row
-// tiles alternate, so the tensor cores work on one while the other's softmax runs; keys and values
-// are read from the cache and converted to binary16 in shared memory once for both.
+// A unit is 256 rows of one (sequence, key head), two tiles of 128, against tiles of 128 slots.  Per step
+// of 64 slots and row tile: S = Q K^T (MMAs M 128, N 64, K 16) into one of two TMEM buffers, softmax by
+// 128 threads with one row each, P as binary16 back into the same buffer, O += P V (P from TMEM).  The
+// scores of a step are there two steps ahead, so the softmax warps need not wait for the tensor cores;
+// keys and values are read from the cache and converted to binary16 in shared memory once for both
+// row tiles.
 //
-// Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 conversion, 12 MMA issue.  The time of a slot
-// tile is bound by three units that are nearly even: the MMAs (4 x 512 cycles), the 32768
-// exponentials (16 a cycle), and shared memory (operand reads of the first product, 64 KB written).
+// Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 conversion, 12 MMA issue.
 //
 // Numerics as in the kernel for few rows (hq_kv8_attend.cu), except that value codes enter binary16
 // multiplied by their page's scale over the largest scale of the segment: exact for power-of-two
@@ -25,6 +24,7 @@ namespace {
 
 constexpr int kThreadsP = 512;
 constexpr int kTok = 128;     // slots of a tile
+constexpr int kStep = 64;     // slots of one step of the softmax: a row tile has two buffers of scores
 constexpr int kPoly = 1, kPolyOf = 2;  // pairs of exponentials on the multiply-add pipe, of so many
 constexpr int kScaleRing = 4;  // tiles whose key scales are kept: the converter is at most two ahead
 
@@ -75,7 +75,8 @@ struct PrefillSmem {
     float red[4];
     alignas(8) uint64_t k_full[2];
     uint64_t k_empty[2], v_full[2], v_empty[2];
-    uint64_t s_full[2], p_ready[2], o_full[2];  // by row tile
+    uint64_t s_full[2][2], p_ready[2][2];  // by row tile and score buffer
+    uint64_t pv_done[2], o_full[2];        // by row tile
     uint64_t q_ready[2], drain;
     uint32_t tmem_base;
     uint32_t status;
@@ -136,8 +137,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_full[i], 4);
             mbar_init(&sm.v_empty[i], 1);
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_ready[i], 4);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&sm.s_full[i][j], 1);
+                mbar_init(&sm.p_ready[i][j], 4);
+            }
+            mbar_init(&sm.pv_done[i], 1);
             mbar_init(&sm.o_full[i], 1);
             mbar_init(&sm.q_ready[i], 4);
         }
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lanes + 128 * t, to = lanes + 256 + 128 * t;
-        uint32_t seg_n = 0, tile_n = 0, s_n = 0;  // segments, slot tiles, and this row tile's scores so far
+        uint32_t seg_n = 0, tile_n = 0, s_n = 0, pv_n = 0;  // segments and slot tiles, and those and the steps of this row tile
         while (w0 < w1) {
             const Segment g = segment_at<ManyRows>(a, pre, w0, w1);
             const int row = g.rt * kManyRows + t * 128 + r, i = row / a.G;
@@ -209,55 +213,43 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
             const int T = (int)(g.t1 - g.t0);
             if (active) {
 #pragma unroll 1
-                for (int j = 0; j < T; ++j) {
-                    const int tok = (int)(g.t0 + j) * kTok;
-                    wait(&sm.s_full[t], s_n + j);
+                for (int i2 = 0; i2 < 2 * T; ++i2) {
+                    const int tok = (int)g.t0 * kTok + i2 * kStep, buf = i2 & 1;
+                    const uint32_t tb = ts + kStep * buf;
+                    wait(&sm.s_full[t][buf], s_n + (i2 >> 1));
                     if (!alive) continue;
                     tc_fence_after();
-                    const float* ks = sm.ks[(tile_n + j) % kScaleRing];
-                    if (tok + kTok > full_end || __any_sync(0xFFFFFFFFu, ks[lane & 7] < 0.0f)) {
-                        // a tile with slots that some row does not see, or whose page is missing: their scores
-                        // become -infinity where they lie, so that the passes below know no masks
-#pragma unroll 1
-                        for (int p = 0; p < 4; ++p) {
-                            uint32_t x[32];
-                            tmem_ld32_nowait(ts + 32 * p, x);
-                            tmem_wait_ld();
-                            const bool no0 = ks[2 * p] < 0.0f, no1 = ks[2 * p + 1] < 0.0f;
-                            const int left = end - tok - 32 * p;
-#pragma unroll
-                            for (int y = 0; y < 32; ++y)
-                                if (y >= left || (y < 16 ? no0 : no1)) x[y] = 0xFF800000u;
-                            tmem_st32(ts + 32 * p, x);
-                        }
-                        tmem_wait_st();
-                    }
-                    // twice over the scores, 32 at a time with the next 32 on their way: keeping all 128 would
-                    // take the registers of a third warpgroup
                     uint32_t S[2][32];
-                    tmem_ld32_nowait(ts, S[0]);
-                    float top = -INFINITY;
+                    tmem_ld32_nowait(tb, S[0]);
+                    tmem_ld32_nowait(tb + 32, S[1]);
+                    const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[(tile_n + (i2 >> 1)) % kScaleRing][4 * buf]);
+                    tmem_wait_ld();
+                    if (tok + kStep > full_end || fminf(fminf(ks.x, ks.y), fminf(ks.z, ks.w)) < 0.0f) {
+                        // slots that some row does not see, or whose page is missing
+                        const int left = end - tok;
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        tmem_wait_ld();
-                        tmem_ld32_nowait(ts + 32 * ((p + 1) & 3), S[(p + 1) & 1]);
-                        const float k0 = ks[2 * p], k1 = ks[2 * p + 1];
-                        float x[8];
-#pragma unroll
-                        for (int z = 0; z < 8; ++z) x[z] = __uint_as_float(S[p & 1][4 * z]);
-#pragma unroll
-                        for (int y = 1; y < 4; ++y)
-#pragma unroll
-                            for (int z = 0; z < 8; ++z) x[z] = fmaxf(x[z], __uint_as_float(S[p & 1][4 * z + y]));
-                        const float x0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), x1 = fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]));
-                        top = fmaxf(top, fmaxf(x0 * (c * fabsf(k0)), x1 * (c * fabsf(k1))));
+                        for (int y = 0; y < kStep; ++y)
+                            if (y >= left || (y < 16 ? ks.x : (y < 32 ? ks.y : (y < 48 ? ks.z : ks.w))) < 0.0f) S[y >> 5][y & 31] = 0xFF800000u;
                     }
+                    const float cg[4] = {c * fabsf(ks.x), c * fabsf(ks.y), c * fabsf(ks.z), c * fabsf(ks.w)};
+                    float x[8];
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) x[z] = __uint_as_float(S[z >> 2][(z & 3) * 8]);
+#pragma unroll
+                    for (int y = 1; y < 8; ++y)
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) x[z] = fmaxf(x[z], __uint_as_float(S[z >> 2][(z & 3) * 8 + y]));
+                    const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]) * cg[0], fmaxf(x[2], x[3]) * cg[1]),
+                                            fmaxf(fmaxf(x[4], x[5]) * cg[2], fmaxf(x[6], x[7]) * cg[3]));
                     const bool moves = top > m + kSlack;
                     if (__any_sync(0xFFFFFFFFu, moves)) {
                         const float next = moves ? top : m, f = m == -INFINITY ? 1.0f : ex2(m - next);
                         l *= f;
                         m = next;
-                        if (j > 0) {  // the accumulator's products so far are done: this tile's scores came after them
+                        if (i2 > 0) {  // once the products before this step's are done
+                            wait(&sm.pv_done[t], pv_n + i2 - 1);
+                            if (!alive) continue;
+                            tc_fence_after();
 #pragma unroll 1
                             for (int p = 0; p < D / 32; ++p) {
                                 uint32_t o[32];
@@ -273,29 +265,25 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     const float2 nsub = make_float2(-sub, -sub);
                     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        tmem_wait_ld();
-                        if (p < 3) tmem_ld32_nowait(ts + 32 * (p + 1), S[(p + 1) & 1]);
-                        const float k0 = ks[2 * p], k1 = ks[2 * p + 1];
-                        const float c0 = c * fabsf(k0), c1 = c * fabsf(k1);
+                    for (int p = 0; p < 2; ++p) {
                         uint32_t P[16];
 #pragma unroll
                         for (int y = 0; y < 16; ++y) {
-                            const float cq = y < 8 ? c0 : c1;
-                            float2 x = __ffma2_rn(make_float2(__uint_as_float(S[p & 1][2 * y]), __uint_as_float(S[p & 1][2 * y + 1])),
+                            const float cq = cg[2 * p + (y >> 3)];
+                            float2 e = __ffma2_rn(make_float2(__uint_as_float(S[p][2 * y]), __uint_as_float(S[p][2 * y + 1])),
                                                   make_float2(cq, cq), nsub);
-                            if (y % kPolyOf < kPoly) x = exp2_poly(x);
-                            else x = make_float2(ex2(x.x), ex2(x.y));
-                            sum = f2add(sum, x);
-                            P[y] = pack_f16(x.x, x.y);
+                            if (y % kPolyOf < kPoly) e = exp2_poly(e);
+                            else e = make_float2(ex2(e.x), ex2(e.y));
+                            sum = f2add(sum, e);
+                            P[y] = pack_f16(e.x, e.y);
                         }
-                        tmem_st16(ts + 16 * p, P);
+                        tmem_st16(tb + 16 * p, P);
                     }
                     l += sum.x + sum.y;
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_ready[t]);
+                    if (lane == 0) mbar_arrive(&sm.p_ready[t][buf]);
                 }
                 if (m == -INFINITY) l = 0.0f;  // no slot seen: not even the polynomial's smallest value
                 // the segment's accumulator
@@ -342,6 +330,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     tc_fence_before();
                 }
                 s_n += T;
+                pv_n += 2 * T;
             } else {
                 wait(&sm.o_full[t], seg_n);  // without rows: keep step with the others, one segment at a time
             }
@@ -444,18 +433,20 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
     } else {
         if (warp == 12) {
             // ---------------- MMA issue ----------------
-            constexpr uint32_t IDS = idesc_f16(128, 128, false), IDO = idesc_f16(128, D, true);
+            constexpr uint32_t IDS = idesc_f16(128, kStep, false), IDO = idesc_f16(128, D, true);
             uint32_t seg_n = 0, tile_n = 0, s_n[2] = {0, 0};
             // operand tiles follow one another: descriptors differ by their distance in 16-byte units
             constexpr uint64_t RUN = Smem::HALF >> 4, TILE = (D / 64) * RUN;
             const uint64_t dq = sw128_desc(sm.q[0][0]), dk = sw128_desc(sm.k[0][0]), dv = sw128_desc_mn(sm.v[0][0], Smem::HALF);
-            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0);
-            auto score = [&](int t, int st) {
-                const uint64_t ad = dq + (t ? TILE : 0), bd = dk + (st ? TILE : 0);
+            const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), leader = elect_lane();
+            // step i of the segment, half `i & 1` of slot tile `st`, into score buffer i & 1
+            constexpr uint64_t HALFTILE = (kStep * 128) >> 4;
+            auto score = [&](int t, int st, int buf) {
+                const uint64_t ad = dq + (t ? TILE : 0), bd = dk + (st ? TILE : 0) + (buf ? HALFTILE : 0);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    mma_f16_ss(tb + 128 * t, ad + (kk >> 2) * RUN + 2 * (kk & 3), bd + (kk >> 2) * RUN + 2 * (kk & 3), IDS, kk > 0);
-                mma_commit_warp(&sm.s_full[t]);
+                    mma_f16_ss(tb + 128 * t + kStep * buf, ad + (kk >> 2) * RUN + 2 * (kk & 3), bd + (kk >> 2) * RUN + 2 * (kk & 3), IDS, kk > 0, leader);
+                mma_commit_warp(&sm.s_full[t][buf], leader);
             };
             while (w0 < w1) {
                 const Segment g = segment_at<ManyRows>(a, pre, w0, w1);
@@ -466,37 +457,48 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                 wait(&sm.k_full[tile_n & 1], tile_n / 2);
                 tc_fence_after();
                 if (alive) {
-                    for (int t = 0; t < nt; ++t) score(t, tile_n & 1);
-                    mma_commit_warp(&sm.k_empty[tile_n & 1]);
+#pragma unroll
+                    for (int buf = 0; buf < 2; ++buf)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            if (t < nt) score(t, tile_n & 1, buf);
+                    mma_commit_warp(&sm.k_empty[tile_n & 1], leader);
                 }
 #pragma unroll 1
                 for (int j = 0; j < T; ++j, ++tile_n) {
                     const int st = tile_n & 1, next = st ^ 1;
                     wait(&sm.v_full[st], tile_n / 2);
-                    for (int t = 0; t < nt; ++t) {
-                        wait(&sm.p_ready[t], s_n[t]++);
-                        if (t == 0 && j + 1 < T) wait(&sm.k_full[next], (tile_n + 1) / 2);
-                        tc_fence_after();
-                        if (!alive) continue;
+                    if (j + 1 < T) wait(&sm.k_full[next], (tile_n + 1) / 2);
 #pragma unroll
-                        for (int kk = 0; kk < kTok / 16; ++kk)
-                            mma_f16_ts(tb + 256 + 128 * t, tb + 128 * t + 8 * kk, dv + (st ? TILE : 0) + (uint64_t)(128 * kk), IDO,
-                                       j > 0 || kk > 0);
-                        if (t == nt - 1) mma_commit_warp(&sm.v_empty[st]);
-                        if (j + 1 < T) {
-                            score(t, next);
-                            if (t == nt - 1) mma_commit_warp(&sm.k_empty[next]);
-                        } else {
-                            mma_commit_warp(&sm.o_full[t]);
-                            if (nt == 1) mma_commit_warp(&sm.o_full[1]);
+                    for (int buf = 0; buf < 2; ++buf)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (t >= nt) continue;
+                            wait(&sm.p_ready[t][buf], s_n[t]);
+                            tc_fence_after();
+                            if (!alive) continue;
+#pragma unroll
+                            for (int kk = 0; kk < kStep / 16; ++kk)
+                                mma_f16_ts(tb + 256 + 128 * t, tb + 128 * t + kStep * buf + 8 * kk,
+                                           dv + (st ? TILE : 0) + (buf ? HALFTILE : 0) + (uint64_t)(128 * kk), IDO, j > 0 || buf > 0 || kk > 0, leader);
+                            mma_commit_warp(&sm.pv_done[t], leader);
+                            if (buf && t == nt - 1) mma_commit_warp(&sm.v_empty[st], leader);
+                            if (j + 1 < T) {  // the scores of two steps on take this step's buffer
+                                score(t, next, buf);
+                                if (buf && t == nt - 1) mma_commit_warp(&sm.k_empty[next], leader);
+                            } else if (buf) {
+                                mma_commit_warp(&sm.o_full[t], leader);
+                                if (nt == 1) mma_commit_warp(&sm.o_full[1], leader);
+                            }
                         }
-                    }
+                    ++s_n[0];
+                    if (nt == 2) ++s_n[1];
                 }
                 ++seg_n;
                 w0 += T;
             }
             // nothing may be under way when the tensor memory is given back
-            mma_commit_warp(&sm.drain);
+            mma_commit_warp(&sm.drain, leader);
             mbar_wait_sleep(&sm.drain, 0);
             __syncwarp();
         }

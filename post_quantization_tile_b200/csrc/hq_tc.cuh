@@ -50,48 +50,54 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
 // The wrappers below are called by a whole converged warp, one elected lane of which issues: descriptors
 // and addresses are then the warp's own (uniform) values.  Issued from a branch that only one lane takes,
 // each MMA first collected its operands from that lane's registers, which took longer than the MMA.
+// `leader`: elect_lane() of the warp, taken once.
+__device__ __forceinline__ uint32_t elect_lane()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\tselp.u32 %0, 1, 0, one;\n\t}\n" : "=r"(r));
+    return r;
+}
 
 // arrive on `bar` once every MMA issued so far by the warp's elected lane has completed
-__device__ __forceinline__ void mma_commit_warp(uint64_t* bar)
+__device__ __forceinline__ void mma_commit_warp(uint64_t* bar, uint32_t leader)
 {
-    asm volatile("{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+    asm volatile("{\n\t.reg .pred one;\n\tsetp.ne.b32 one, %1, 0;\n\t"
                  "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
-                 ::"r"(smem_u32(bar))
+                 ::"r"(smem_u32(bar)), "r"(leader)
                  : "memory");
 }
 
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t leader)
 {
-    const uint32_t z = 0u;
     asm volatile(
         "{\n\t.reg .pred p, one;\n\t"
-        "elect.sync _|one, 0xffffffff;\n\t"
+        "setp.ne.b32 one, %5, 0;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "@one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}\n"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(z), "r"(z), "r"(z), "r"(z)
+        "@one tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
 // D (TMEM) (+)= A (shared memory) B (shared memory), binary16 in, binary32 out
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
         "{\n\t.reg .pred p, one;\n\t"
-        "elect.sync _|one, 0xffffffff;\n\t"
+        "setp.ne.b32 one, %5, 0;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 // the same with A in TMEM (two binary16 of a row per column)
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
         "{\n\t.reg .pred p, one;\n\t"
-        "elect.sync _|one, 0xffffffff;\n\t"
+        "setp.ne.b32 one, %5, 0;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
@@ -145,22 +151,22 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
         "{\n\t.reg .pred p, one;\n\t"
-        "elect.sync _|one, 0xffffffff;\n\t"
+        "setp.ne.b32 one, %5, 0;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "@one tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 // arrive on `bar` of both CTAs once every MMA issued so far by the warp's elected lane has completed
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar)
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t leader)
 {
-    asm volatile("{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+    asm volatile("{\n\t.reg .pred one;\n\tsetp.ne.b32 one, %2, 0;\n\t"
                  "@one tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n"
-                 ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)3), "r"(leader)
                  : "memory");
 }
 
