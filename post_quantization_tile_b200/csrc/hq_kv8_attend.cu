@@ -2,25 +2,28 @@
 //
 //   s_rj = scale q_r . k_j,  out_r = sum_j exp(s_rj) v_j / sum_j exp(s_rj) over the visible slots j
 //
-// One pass over the keys and values with a running maximum and sum.  The rows r of one (sequence,
-// key head) are its queries times the query heads of the group; sixteen of them make one unit, and
-// all of them share the keys and values that a warp loads.  The units' tokens, in tiles of 64, are
+// One pass over the keys and values with a running reference and sum.  The rows r of one (sequence,
+// key head) are its queries times the query heads of the group; eight or sixteen of them make one
+// unit, and all of them share the keys and values that a warp loads.  The units' slots, in tiles of 64, are
 // laid end to end and cut into equal shares, one per resident thread block, so ragged batches and
-// single long sequences fill the GPU alike; where a unit is cut, the parts leave their maximum, sum and
+// single long sequences fill the GPU alike; where a unit is cut, the parts leave their reference, sum and
 // accumulator in the workspace and a second small kernel joins them.
 //
 // Codes become binary16 in registers (one conversion instruction for two codes, exact) and both
-// products run on the matrix instruction m16n8k16 with binary32 accumulators.  Sixteen tokens of one
-// head are contiguous (a page holds a multiple of sixteen), so every warp streams its groups of
-// sixteen keys and values with two TMA boxes each into a ring of its own, without any barrier between
-// warps.  The order of the contraction and of the output columns is free: every lane reads 16
-// contiguous bytes of a key or value row as the fragments it needs, the boxes' swizzle keeps those
-// reads free of bank conflicts, and nothing is transposed but byte pairs of two value rows.
+// products run on the matrix instruction m16n8k16 with binary32 accumulators, keys and values on the
+// wide side: S^T = K Q^T (sixteen slots by eight rows), O^T += V^T P^T.  Sixteen slots of one head are
+// contiguous (a page holds a multiple of sixteen), so every warp streams its groups of sixteen keys
+// and values with two TMA boxes each into a ring of its own, without any barrier between warps.  The
+// order of the contraction and of the output is free: every lane reads 16 contiguous bytes of a key or
+// value row as the fragments it needs, the boxes' swizzle keeps those reads free of bank conflicts, and
+// nothing is transposed but byte pairs of two value rows and the 8 x 8 tiles of probabilities
+// (movmatrix).
 //   - queries become binary16 after a power-of-two scaling per row (bf16's 8 bits fit exactly, elements
 //     below 2^-38 of the row's largest lose bits);
 //   - probabilities become binary16 at 2^7 times their value relative to a running reference, which
 //     moves up to the maximum when that is more than 2^8 larger: 11 bits, at most 2^15, and weights
-//     down to 2^-31 of the largest still count;
+//     down to 2^-31 of the largest still count.  The lanes look for a maximum only when one of them
+//     meets a score beyond that;
 //   - key scales multiply the scores, value scales stay out of the products: the accumulator is kept in
 //     units of the last value scale and multiplied by the (power-of-two) ratio when that changes.
 #include <cuda_runtime.h>
@@ -31,12 +34,22 @@ namespace hq {
 namespace {
 
 constexpr int kWarps = 4, kThreadsA = 32 * kWarps;
-constexpr int kStages = 4;  // ring of sixteen-token groups per warp
 
-// units of sixteen rows in tiles of 64 slots; slots that only later rows of a sequence see are part of
+// Rows of a unit, thread blocks of an SM and groups in a warp's ring.  Eight rows take half the registers
+// of sixteen, so twelve warps are resident instead of eight, each with 12 KB of keys and values under
+// way (dim 128).
+template <int ROWS>
+struct FewCfg {
+    static constexpr int NT = ROWS / 8;                 // row tiles of the matrix instruction
+    static constexpr int BLOCKS = ROWS == 8 ? 3 : 2;
+    static constexpr int STAGES = ROWS == 8 ? 3 : 4;
+};
+
+// units of ROWS rows in tiles of 64 slots; slots that only later rows of a sequence see are part of
 // every unit's tiles (at most its queries: few) and skipped
+template <int ROWS>
 struct FewRows {
-    static constexpr int R = 16, TILE = 64;
+    static constexpr int R = ROWS, TILE = 64;
     static __device__ __forceinline__ int row_tiles(const AttendArgs& a, int m) { return (m * a.G + R - 1) / R; }
     static __device__ __forceinline__ uint32_t tiles(const AttendArgs&, const SeqLen& s, int) { return (uint32_t)((s.n + TILE - 1) / TILE); }
     static __device__ __forceinline__ uint32_t of_sequence(const AttendArgs& a, const SeqLen& s)
@@ -58,27 +71,37 @@ struct FewRows {
     }
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&b)[2])
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
+}
+// transposes an 8 x 8 tile of binary16 pairs across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
-// sixteen query rows as the A fragments of the score product, and the factors of their scores
-template <int D>
+// 8 NT query rows as the B fragments of the score product; for the rows 8 i + 2 t + e of this lane's
+// scores, their factor and the slots they see
+template <int D, int NT>
 struct QueryRows {
-    uint32_t f[D / 16][4];
-    float c[2];  // score factor of rows lane / 4 and lane / 4 + 8
-    int end[2];  // slots they see (0: no such row)
+    uint32_t f[NT][D / 16][2];
+    float c[NT][2];
+    int end[NT][2];  // 0: no such row
+    int full;        // slots that all rows see
 
     __device__ __forceinline__ void load(const AttendArgs& a, int b, int h, int rt, const SeqLen& s)
     {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        full = 0x7FFFFFFF;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = rt * 16 + g + 8 * half, i = r / a.G;
+        for (int n = 0; n < NT; ++n) {
+            const int r = (rt * NT + n) * 8 + g, i = r / a.G;
             const bool is = i < s.m;
             const __nv_bfloat16* q = a.q + b * a.qb + (int64_t)(h * a.G + (is ? r - i * a.G : 0)) * a.qh + (is ? i : 0) * a.qs;
             uint2 w[D / 16];
@@ -92,13 +115,18 @@ struct QueryRows {
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
             const int e = m ? min(126, 14 + 127 - (int)(m >> 23)) : 0;
-            const float up = exp2_int(e);
-            c[half] = exp2_int(-e) * a.scale * kLog2e;
-            end[half] = is ? sees(a, s.n, s.m, i) : 0;
+            const float up = exp2_int(e), factor = exp2_int(-e) * a.scale * kLog2e;
+            const int sees_r = is ? sees(a, s.n, s.m, i) : 0;
+            full = min(full, (int)__reduce_min_sync(0xFFFFFFFFu, is ? (uint32_t)sees_r : 0x7FFFFFFFu));
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                c[n][y] = __shfl_sync(0xFFFFFFFFu, factor, 4 * (2 * t + y));
+                end[n][y] = __shfl_sync(0xFFFFFFFFu, sees_r, 4 * (2 * t + y));
+            }
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                f[kk][half] = pack_f16(bf16lo_to_f32(w[kk].x) * up, bf16hi_to_f32(w[kk].x) * up);
-                f[kk][half + 2] = pack_f16(bf16lo_to_f32(w[kk].y) * up, bf16hi_to_f32(w[kk].y) * up);
+                f[n][kk][0] = pack_f16(bf16lo_to_f32(w[kk].x) * up, bf16hi_to_f32(w[kk].x) * up);
+                f[n][kk][1] = pack_f16(bf16lo_to_f32(w[kk].y) * up, bf16hi_to_f32(w[kk].y) * up);
             }
         }
     }
@@ -111,8 +139,7 @@ __device__ __forceinline__ uint32_t swz_row(int r, int c)
     return (uint32_t)(r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
 }
 
-// sixteen tokens' keys: lane (g, t) holds dims t D/4 .. of tokens g and g + 8, whose scores are the
-// columns g of its two score tiles
+// sixteen slots' keys: lane (g, t) holds dims t D/4 .. of slots g and g + 8, the rows of its score tile
 template <int D>
 struct KeyGroup {
     uint4 w[2][D / 64];
@@ -136,23 +163,27 @@ struct KeyGroup {
                 w[i][j] = ok ? __ldg(reinterpret_cast<const uint4*>(k + (g + 8 * i) * D + t * (D / 4) + j * 16))
                              : make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void scores(const QueryRows<D>& q, float (&s)[2][4]) const
+    // s[n]: rows 8 n + 2 t, + 1 against slot g, then against slot g + 8
+    template <int NT>
+    __device__ __forceinline__ void scores(const QueryRows<D, NT>& q, float (&s)[NT][4]) const
     {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const uint32_t x[4] = {w[i][j].x, w[i][j].y, w[i][j].z, w[i][j].w};
+        for (int j = 0; j < D / 64; ++j) {
+            const uint32_t x[4] = {w[0][j].x, w[0][j].y, w[0][j].z, w[0][j].w}, y[4] = {w[1][j].x, w[1][j].y, w[1][j].z, w[1][j].w};
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    mma16816(s[i], q.f[4 * j + y], e4m3x2_to_f16x2(x[y] & 0xFFFFu), e4m3x2_to_f16x2(x[y] >> 16));
+            for (int z = 0; z < 4; ++z) {
+                const uint32_t a0 = e4m3x2_to_f16x2(x[z] & 0xFFFFu), a1 = e4m3x2_to_f16x2(y[z] & 0xFFFFu);
+                const uint32_t a2 = e4m3x2_to_f16x2(x[z] >> 16), a3 = e4m3x2_to_f16x2(y[z] >> 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(s[n], a0, a1, a2, a3, q.f[n][4 * j + z]);
             }
         }
     }
 };
 
-// sixteen tokens' values: lane (g, t) holds dims g D/8 .. of tokens 2 t, 2 t + 1, 2 t + 8 and 2 t + 9
+// sixteen slots' values: lane (g, t) holds dims g D/8 .. of slots 2 t, 2 t + 1, 2 t + 8 and 2 t + 9
 template <int D>
 struct ValueGroup {
     uint32_t w[4][D / 32];
@@ -179,197 +210,213 @@ struct ValueGroup {
                     for (int j = 0; j < D / 32; ++j) w[i][j] = 0u;
         }
     }
-    __device__ __forceinline__ void accumulate(const uint32_t (&p)[4], float (&o)[D / 8][4]) const
+    // o[n][i]: rows 8 n + 2 t, + 1 of dim g D/8 + 2 i, then of dim g D/8 + 2 i + 1
+    template <int NT>
+    __device__ __forceinline__ void accumulate(const uint32_t (&p)[NT][2], float (&o)[NT][D / 16][4]) const
     {
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-            const uint32_t lo0 = __byte_perm(w[0][j], w[1][j], 0x5140), hi0 = __byte_perm(w[0][j], w[1][j], 0x7362);
-            const uint32_t lo1 = __byte_perm(w[2][j], w[3][j], 0x5140), hi1 = __byte_perm(w[2][j], w[3][j], 0x7362);
-            mma16816(o[4 * j], p, e4m3x2_to_f16x2(lo0 & 0xFFFFu), e4m3x2_to_f16x2(lo1 & 0xFFFFu));
-            mma16816(o[4 * j + 1], p, e4m3x2_to_f16x2(lo0 >> 16), e4m3x2_to_f16x2(lo1 >> 16));
-            mma16816(o[4 * j + 2], p, e4m3x2_to_f16x2(hi0 & 0xFFFFu), e4m3x2_to_f16x2(hi1 & 0xFFFFu));
-            mma16816(o[4 * j + 3], p, e4m3x2_to_f16x2(hi0 >> 16), e4m3x2_to_f16x2(hi1 >> 16));
+            const uint32_t x[2] = {__byte_perm(w[0][j], w[1][j], 0x5140), __byte_perm(w[0][j], w[1][j], 0x7362)};
+            const uint32_t y[2] = {__byte_perm(w[2][j], w[3][j], 0x5140), __byte_perm(w[2][j], w[3][j], 0x7362)};
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const uint32_t a0 = e4m3x2_to_f16x2(x[z] & 0xFFFFu), a1 = e4m3x2_to_f16x2(x[z] >> 16);
+                const uint32_t a2 = e4m3x2_to_f16x2(y[z] & 0xFFFFu), a3 = e4m3x2_to_f16x2(y[z] >> 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(o[n][2 * j + z], a0, a1, a2, a3, p[n]);
+            }
         }
     }
 };
 
-template <int D>
+template <int D, int ROWS>
 struct AttendSmem {
-    unsigned char ring[kWarps][kStages][2][16 * D];  // keys, values of a group (TMA boxes: 1024-byte aligned)
-    float o[kWarps][16][D + 4];
-    float m[kWarps][16], l[kWarps][16];
-    float2 scale[kWarps][kStages];  // of the group's keys and values; values < 0: no such page
-    uint64_t full[kWarps][kStages];
+    static constexpr int STAGES = FewCfg<ROWS>::STAGES;
+    unsigned char ring[kWarps][STAGES][2][16 * D];  // keys, values of a group (TMA boxes: 1024-byte aligned)
+    float o[kWarps][ROWS][D + 4];
+    float m[kWarps][ROWS], l[kWarps][ROWS];
+    float2 scale[kWarps][STAGES];  // of the group's keys and values; values < 0: no such page
+    uint64_t full[kWarps][STAGES];
     uint32_t scan[kWarps];
     uint32_t status;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsA, 2)
+constexpr float kNoReference = -3e38f;  // below every score: the first visible one moves it
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
     kv8_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv)
 {
+    constexpr int NT = FewCfg<ROWS>::NT, STAGES = FewCfg<ROWS>::STAGES;
+    using U = FewRows<ROWS>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    AttendSmem<D>& sm = *reinterpret_cast<AttendSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    using Smem = AttendSmem<D, ROWS>;
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint32_t* pre = reinterpret_cast<uint32_t*>(&sm + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (tid == 0) {
         sm.status = 0u;
         for (int w = 0; w < kWarps; ++w)
-            for (int i = 0; i < kStages; ++i) mbar_init(&sm.full[w][i], 1);
+            for (int i = 0; i < STAGES; ++i) mbar_init(&sm.full[w][i], 1);
         fence_mbar_init();
     }
-    if (share_prefix<FewRows, kThreadsA>(a, pre, sm.scan) && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
+    if (share_prefix<U, kThreadsA>(a, pre, sm.scan) && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
     const uint32_t W = pre[a.B];
     const uint32_t shares = min(W, gridDim.x);  // none is empty: the join walks a unit's shares one by one
     uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
     const uint32_t w1 = blockIdx.x < shares ? (uint32_t)((uint64_t)(blockIdx.x + 1) * W / shares) : 0u;
     uint32_t status = 0u;
     bool dead = false;  // after a timeout a warp only walks the loops, so that all reach the barriers
-    uint32_t it = 0;  // groups this warp has issued before this unit: ring stage and parity
+    uint32_t stage = 0, parity = 0;  // of the next group this warp waits for
     while (w0 < w1) {
-        const Segment seg = segment_at<FewRows>(a, pre, w0, w1);
+        const Segment seg = segment_at<U>(a, pre, w0, w1);
         const SeqLen s = seg.s;
         const int b = seg.b, h = seg.h, rt = seg.rt;
         const uint32_t t0 = seg.t0, t1 = seg.t1, tiles = seg.tiles;
-        const int last_row = min(rt * 16 + 15, s.m * a.G - 1);
-        const int end = min((int)t1 * FewRows::TILE, sees(a, s.n, s.m, last_row / a.G));
-        const int groups = (end + 15) / 16;  // sixteen-token groups up to the last visible slot
+        const int last_row = min(rt * ROWS + ROWS - 1, s.m * a.G - 1);
+        const int end = min((int)t1 * U::TILE, sees(a, s.n, s.m, last_row / a.G));
+        const int groups = (end + 15) / 16;  // sixteen-slot groups up to the last visible slot
         const int32_t* table = a.table + b * a.table_stride;
 
-        QueryRows<D> q;
-        q.load(a, b, h, rt, s);
-        float o[D / 8][4];
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, vref = 1.0f;
-
         // this warp's groups: every kWarps-th; their page rows and scales are fetched 32 at a time, one
-        // per lane, and the boxes of kStages groups are under way at any time
-        const int gr0 = (int)t0 * (FewRows::TILE / 16) + warp, count = gr0 < groups && !dead ? (groups - gr0 + kWarps - 1) / kWarps : 0;
+        // per lane, and the boxes of STAGES groups are under way at any time
+        const int gr0 = (int)t0 * (U::TILE / 16) + warp, count = gr0 < groups && !dead ? (groups - gr0 + kWarps - 1) / kWarps : 0;
         int my_row = -1;
         float2 my_scale = make_float2(0.0f, -1.0f);
-        auto issue = [&](int i) {
+        auto issue = [&](int i, uint32_t st) {
             if ((i & 31) == 0) {
                 my_row = i + lane < count ? locate(a, table, h, (gr0 + (i + lane) * kWarps) * 16) : -1;
+                my_scale.y = -1.0f;
                 if (my_row >= 0) {
                     const int ph = my_row >> a.page_shift;
                     my_scale = make_float2(__ldg(a.c.k_scale + ph), __ldg(a.c.v_scale + ph));
-                } else {
-                    my_scale.y = -1.0f;
-                    if (i + lane < count) status |= kStRange;
+                } else if (i + lane < count) {
+                    status |= kStRange;
                 }
             }
-            const int row = __shfl_sync(0xFFFFFFFFu, my_row, i & 31);
-            const float ks = __shfl_sync(0xFFFFFFFFu, my_scale.x, i & 31), vs = __shfl_sync(0xFFFFFFFFu, my_scale.y, i & 31);
-            if (lane == 0) {
-                const uint32_t st = (it + i) % kStages;
-                sm.scale[warp][st] = make_float2(ks, vs);
-                if (row >= 0) {
+            if (lane == (i & 31)) {  // the lane that knows the group issues it
+                sm.scale[warp][st] = my_scale;
+                if (my_row >= 0) {
                     mbar_arrive_expect_tx(&sm.full[warp][st], 32 * D);
-                    tma_load_2d(sm.ring[warp][st][0], &tk, 0, row, &sm.full[warp][st]);
-                    tma_load_2d(sm.ring[warp][st][1], &tv, 0, row, &sm.full[warp][st]);
+                    tma_load_2d(sm.ring[warp][st][0], &tk, 0, my_row, &sm.full[warp][st]);
+                    tma_load_2d(sm.ring[warp][st][1], &tv, 0, my_row, &sm.full[warp][st]);
                 } else {
                     mbar_arrive(&sm.full[warp][st]);
                 }
             }
         };
-        for (int i = 0; i < kStages && i < count; ++i) issue(i);
+        {
+            uint32_t st = stage;
+            for (int i = 0; i < STAGES && i < count; ++i) {
+                issue(i, st);
+                st = st + 1 == STAGES ? 0 : st + 1;
+            }
+        }
+        QueryRows<D, NT> q;
+        q.load(a, b, h, rt, s);
+        float o[NT][D / 16][4], sub[NT][2], l[NT][2], vref = 1.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
+            sub[n][0] = sub[n][1] = kNoReference;
+            l[n][0] = l[n][1] = 0.0f;
+        }
         __syncwarp();
         for (int i = 0; i < count; ++i) {
-            const uint32_t st = (it + i) % kStages;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][st], ((it + i) / kStages) & 1))) {
-                status |= kStTimeout;  // the copies of the other stages are waited for below
-                for (int j = i + 1; j < count && j < i + kStages; ++j)
-                    mbar_wait(&sm.full[warp][(it + j) % kStages], ((it + j) / kStages) & 1);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][stage], parity))) {
+                status |= kStTimeout;
+                for (int j = i + 1; j < count && j < i + STAGES; ++j) {  // the copies of the other stages land first
+                    stage = stage + 1 == STAGES ? 0 : stage + 1;
+                    parity ^= stage == 0;
+                    mbar_wait(&sm.full[warp][stage], parity);
+                }
                 dead = true;
                 break;
             }
             const int tok = (gr0 + i * kWarps) * 16;
-            const float ks = sm.scale[warp][st].x, vs = sm.scale[warp][st].y;
+            const float ks = sm.scale[warp][stage].x, vs = sm.scale[warp][stage].y;
             KeyGroup<D> k;
             ValueGroup<D> v;
-            k.load(sm.ring[warp][st][0]);
-            v.load(sm.ring[warp][st][1], end - tok);
+            k.load(sm.ring[warp][stage][0]);
+            v.load(sm.ring[warp][stage][1], end - tok);
             __syncwarp();  // the stage is in registers: fill it again
-            if (i + kStages < count) issue(i + kStages);
+            if (i + STAGES < count) issue(i + STAGES, stage);
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            parity ^= stage == 0;
             if (vs < 0.0f) continue;
-            float x[2][4];
-            k.scores(q, x);
-            float top[2];
+            float x[NT][4], y[NT][4];
+            k.scores(q, y);
+            const bool edge = tok + 16 > q.full;
+            float top = -INFINITY;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float c = q.c[half] * ks;
-                const int left = q.end[half] - tok;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        x[i][2 * half + e] = 2 * t + 8 * i + e < left ? x[i][2 * half + e] * c : -INFINITY;
-                top[half] = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
-                top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
-                top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 2));
-            }
+                for (int e = 0; e < 4; ++e) {
+                    y[n][e] *= q.c[n][e & 1] * ks;
+                    if (edge && tok + g + 8 * (e >> 1) >= q.end[n][e & 1]) y[n][e] = -INFINITY;
+                    x[n][e] = y[n][e] - sub[n][e & 1];
+                    top = fmaxf(top, x[n][e]);
+                }
             // a reference that moves or another value scale changes the accumulator's units
-            const bool moves = top[0] > m[0] + kSlack || top[1] > m[1] + kSlack || vs != vref;
-            if (__any_sync(0xFFFFFFFFu, moves)) {
+            if (__any_sync(0xFFFFFFFFu, top > kBoost + kSlack || vs != vref)) {
                 const float vr = __fdiv_rn(vref, vs);
-                float f[2];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    top[half] = top[half] > m[half] + kSlack ? top[half] : m[half];
-                    f[half] = m[half] == -INFINITY ? 1.0f : ex2(m[half] - top[half]);
-                    l[half] *= f[half];
-                    f[half] *= vr;
-                    m[half] = top[half];
-                }
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][0] *= f[0];
-                    o[j][1] *= f[0];
-                    o[j][2] *= f[1];
-                    o[j][3] *= f[1];
-                }
-                vref = vs;
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float sub = m[half] == -INFINITY ? 0.0f : m[half] - kBoost;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        x[i][2 * half + e] = ex2(x[i][2 * half + e] - sub);
-                        l[half] += x[i][2 * half + e];
+                        float best = fmaxf(y[n][e], y[n][e + 2]);
+#pragma unroll
+                        for (int z = 4; z < 32; z <<= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, z));
+                        const float next = best - kBoost > sub[n][e] + kSlack ? best - kBoost : sub[n][e];
+                        const float f = ex2(sub[n][e] - next);
+                        sub[n][e] = next;
+                        l[n][e] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            o[n][j][e] *= f * vr;
+                            o[n][j][e + 2] *= f * vr;
+                        }
+                        x[n][e] = y[n][e] - next;
+                        x[n][e + 2] = y[n][e + 2] - next;
                     }
+                vref = vs;
             }
-            const uint32_t p[4] = {pack_f16(x[0][0], x[0][1]), pack_f16(x[0][2], x[0][3]), pack_f16(x[1][0], x[1][1]),
-                                   pack_f16(x[1][2], x[1][3])};
+            uint32_t p[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[n][e] = ex2(x[n][e]);
+                    l[n][e & 1] += x[n][e];
+                }
+                p[n][0] = transpose8(pack_f16(x[n][0], x[n][1]));
+                p[n][1] = transpose8(pack_f16(x[n][2], x[n][3]));
+            }
             v.accumulate(p, o);
         }
 
-        it += count;
-
-        // join the warps: their accumulators through shared memory, each at the common maximum
+        // join the warps: their accumulators through shared memory, each at the common reference
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 1);
-            l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 2);
-            if (t == 0) {
-                sm.m[warp][g + 8 * half] = m[half];
-                sm.l[warp][g + 8 * half] = l[half];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * n + 2 * t + e;
+#pragma unroll
+                for (int z = 4; z < 32; z <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], z);
+                if (g == 0) {
+                    sm.m[warp][r] = sub[n][e] == kNoReference ? -INFINITY : sub[n][e] + kBoost;
+                    sm.l[warp][r] = l[n][e];
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; j += 2)
+                    *reinterpret_cast<float4*>(&sm.o[warp][r][g * (D / 8) + 2 * j]) =
+                        make_float4(o[n][j][e] * vref, o[n][j][e + 2] * vref, o[n][j + 1][e] * vref, o[n][j + 1][e + 2] * vref);
             }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int j = 0; j < D / 8; j += 4)
-                    *reinterpret_cast<float4*>(&sm.o[warp][g + 8 * half][(2 * t + e) * (D / 8) + j]) =
-                        make_float4(o[j][2 * half + e] * vref, o[j + 1][2 * half + e] * vref, o[j + 2][2 * half + e] * vref,
-                                    o[j + 3][2 * half + e] * vref);
-        }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == tiles;
         const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-        constexpr int TPR = kThreadsA / 16, DPT = D / TPR;  // threads of a row, dims of a thread
+        constexpr int TPR = kThreadsA / ROWS, DPT = D / TPR;  // threads of a row, dims of a thread
         const int r = tid / TPR, d0 = (tid % TPR) * DPT;
         float M = -INFINITY, f[kWarps], L = 0.0f;
 #pragma unroll
@@ -379,7 +426,7 @@ __global__ void __launch_bounds__(kThreadsA, 2)
             f[w] = sm.m[w][r] == -INFINITY ? 1.0f : ex2(sm.m[w][r] - M);
             L += sm.l[w][r] * f[w];
         }
-        const int rr = rt * 16 + r;
+        const int rr = rt * ROWS + r;
         if (!whole || rr < s.m * a.G) {
             const float inv = whole ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
             int head, i;
@@ -387,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsA, 2)
             __nv_bfloat16* out = a.out + b * a.ob + head * a.oh + (int64_t)i * a.os;
             if (d0 == 0) {
                 if (whole) write_lse(a, b, h, rr, M, L);
-                else a.part_ml[slot * 16 + r] = make_float2(M, L);
+                else a.part_ml[slot * ROWS + r] = make_float2(M, L);
             }
 #pragma unroll
             for (int d = 0; d < DPT; d += 4) {
@@ -402,7 +449,7 @@ __global__ void __launch_bounds__(kThreadsA, 2)
                     *reinterpret_cast<uint2*>(out + d0 + d) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                 } else {
-                    *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * 16 + r) * D + d0 + d) = y;
+                    *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * ROWS + r) * D + d0 + d) = y;
                 }
             }
         }
@@ -415,8 +462,8 @@ __global__ void __launch_bounds__(kThreadsA, 2)
 }
 
 // The weight each cached slot received, summed over a key head's rows: with the rows' sums known,
-// exp(s - lse) is recomputed from the keys.  One warp takes sixteen slots and walks the row tiles, so
-// every slot is summed by one lane group in a fixed order.
+// exp(s - lse) is recomputed from the keys.  One warp takes sixteen slots and walks the rows sixteen at a
+// time, so every slot is summed by four lanes in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendArgs a)
 {
@@ -431,46 +478,39 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
     KeyGroup<D> k;
     k.load_global(a.c.k + (int64_t)(ok ? row : 0) * D, ok);
     const float ks = ok ? __ldg(a.c.k_scale + (row >> a.page_shift)) : 0.0f;
-    float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+    float sum[2] = {0.0f, 0.0f};
     const float* lse2 = a.lse2 + ((int64_t)b * a.c.heads + h) * a.G * a.Sq;
-    const int rts = FewRows::row_tiles(a, s.m);
-    for (int rt = 0; rt < rts; ++rt) {
-        QueryRows<D> q;
+    const int rows = s.m * a.G;
+    for (int rt = 0; rt * 16 < rows && ok; ++rt) {
+        QueryRows<D, 2> q;
         q.load(a, b, h, rt, s);
         float x[2][4];
         k.scores(q, x);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const float c = q.c[half] * ks;
-            const int r = rt * 16 + g + 8 * half, left = ok ? q.end[half] - tok : 0;
-            const float l2 = r < s.m * a.G ? lse2[r] : 0.0f;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (2 * t + 8 * i + e < left) sum[i][e] += ex2(x[i][2 * half + e] * c - l2);
-        }
+            for (int e = 0; e < 4; ++e) {
+                const int r = rt * 16 + 8 * i + 2 * t + (e & 1);
+                if (tok + g + 8 * (e >> 1) < q.end[i][e & 1]) sum[e >> 1] += ex2(x[i][e] * (q.c[i][e & 1] * ks) - lse2[r]);
+            }
     }
     const float* win = a.win ? a.win + b * a.wib + h * a.wih : nullptr;
     float* w = a.w + b * a.wb + h * a.wh;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float x = sum[i][e];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-            const int j = tok + 2 * t + 8 * i + e;
-            if (g == 0 && j < n) w[j] = win ? win[j] + x : x;
-        }
+    for (int i = 0; i < 2; ++i) {
+        float x = sum[i];
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+        const int j = tok + g + 8 * i;
+        if (t == 0 && j < n) w[j] = win ? win[j] + x : x;
+    }
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The kernel for many rows (tensor memory, units of 256 rows) reads the cache once for all of them; this
 // one once for every sixteen, from L2.  One unit of sixteen rows: this one.
-bool many_rows(int64_t rows) { return rows > FewRows::R; }
-int attend_grid(bool many) { return many ? num_sms() : 2 * num_sms(); }
+bool many_rows(int64_t rows) { return rows > 16; }
 constexpr int kMaxGridFew = 512, kMaxGridMany = 256;
 
 struct AttendLayout {
@@ -478,7 +518,7 @@ struct AttendLayout {
 };
 AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool weights, bool many)
 {
-    const size_t parts = many ? (size_t)2 * kMaxGridMany * kManyRows : (size_t)2 * kMaxGridFew * FewRows::R;
+    const size_t parts = many ? (size_t)2 * kMaxGridMany * kManyRows : (size_t)2 * kMaxGridFew * 16;
     AttendLayout l;
     l.prefix = align256(kSlotBytes);
     l.part_o = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 1));
@@ -488,27 +528,30 @@ AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool we
     return l;
 }
 
+template <int D, int ROWS>
+cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
+{
+    CUtensorMap tk, tv;
+    const int64_t rows = a.c.pages * a.c.heads * a.c.page;
+    if (!tensor_map_kv8(&tk, a.c.k, rows, D, 16) || !tensor_map_kv8(&tv, a.c.v, rows, D, 16)) return cudaErrorInvalidValue;
+    const size_t smem = 1024 + sizeof(AttendSmem<D, ROWS>) + sizeof(uint32_t) * (size_t)(a.B + 1);
+    cudaError_t e = cudaFuncSetAttribute(kv8_attend_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = min(FewCfg<ROWS>::BLOCKS * num_sms(), kMaxGridFew);
+    kv8_attend_kernel<D, ROWS><<<grid, kThreadsA, smem, st>>>(a, tk, tv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int rts = (a.Sq * a.G + ROWS - 1) / ROWS;
+    kv8_join_kernel<D, FewRows<ROWS>><<<(unsigned)(a.B * a.c.heads * rts), kJoinThreads<ROWS>, 0, st>>>(a, rts, grid);
+    return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_attend(const AttendArgs& a, bool many, cudaStream_t st)
 {
     cudaError_t e;
-    if (many) {
-        const int grid = attend_grid(true) < kMaxGridMany ? attend_grid(true) : kMaxGridMany;
-        if ((e = launch_attend_many(a, grid, st)) != cudaSuccess) return e;
-    } else {
-        CUtensorMap tk, tv;
-        const int64_t rows = a.c.pages * a.c.heads * a.c.page;
-        if (!tensor_map_kv8(&tk, a.c.k, rows, D, 16) || !tensor_map_kv8(&tv, a.c.v, rows, D, 16)) return cudaErrorInvalidValue;
-        const size_t smem = 1024 + sizeof(AttendSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 1);
-        e = cudaFuncSetAttribute(kv8_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        const int grid = attend_grid(false) < kMaxGridFew ? attend_grid(false) : kMaxGridFew;
-        kv8_attend_kernel<D><<<grid, kThreadsA, smem, st>>>(a, tk, tv);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const int rts = (a.Sq * a.G + 15) / 16;
-        kv8_join_kernel<D, FewRows><<<(unsigned)(a.B * a.c.heads * rts), 128, 0, st>>>(a, rts, grid);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
+    if (many) e = launch_attend_many(a, min(num_sms(), kMaxGridMany), st);
+    else e = a.Sq * a.G <= 8 ? launch_few<D, 8>(a, st) : launch_few<D, 16>(a, st);
+    if (e != cudaSuccess) return e;
     if (a.w) {
         const int64_t most = a.slots < a.L ? a.slots : a.L;
         const dim3 wg((unsigned)((most + 16 * kWarps - 1) / (16 * kWarps)), (unsigned)a.c.heads, (unsigned)a.B);
@@ -539,11 +582,11 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     if (p->B < 1 || p->Sq < 1 || p->Hq < H || p->Hq % H || p->max_pages < 1 || p->table_stride < p->max_pages) return HQ_ERR_ARG;
     if (!(p->scale == p->scale) || p->scale - p->scale != 0.0f) return HQ_ERR_ARG;
     if (p->B > kMaxBatch || p->Hq > 65535 || p->Sq > ((int64_t)1 << 24) || p->max_pages > ((int64_t)1 << 24)) return HQ_ERR_UNSUPPORTED;
-    const int64_t G = p->Hq / H, rts = (p->Sq * G + 15) / 16, slots = p->max_pages * page;
+    const int64_t G = p->Hq / H, rts = (p->Sq * G + 7) / 8, slots = p->max_pages * page;
     if (p->cache.pages * H > (((int64_t)1 << 31) - 1) / page) return HQ_ERR_UNSUPPORTED;  // cache rows in 31 bits
     // share units and thread blocks are counted in 31 bits, slots of a sequence too
     if (slots > ((int64_t)1 << 30) || p->Sq * G > ((int64_t)1 << 26) || p->B * H > ((int64_t)1 << 26) ||
-        p->B * H * rts > ((int64_t)1 << 31) / ((slots + FewRows::TILE - 1) / FewRows::TILE))
+        p->B * H * rts > ((int64_t)1 << 31) / ((slots + FewRows<16>::TILE - 1) / FewRows<16>::TILE))
         return HQ_ERR_UNSUPPORTED;
     const int64_t qs = p->q_stride[0] | p->q_stride[1] | p->q_stride[2];
     const int64_t os = p->out_stride[0] | p->out_stride[1] | p->out_stride[2];

@@ -156,15 +156,22 @@ __device__ __forceinline__ Segment segment_at(const AttendArgs& a, const uint32_
     return g;
 }
 
-// Joins the parts of the units that were cut, sixteen rows a thread block, and writes zeros where a row
-// sees nothing.  U: how the attention kernel makes units (U::R rows each) and lays them end to end.
+// Joins the parts of the units that were cut, up to sixteen rows a thread block, eight threads a row, and
+// writes zeros where a row sees nothing.  U: how the attention kernel makes units (U::R rows each) and
+// lays them end to end.
+template <int ROWS>
+constexpr int kJoinRows = ROWS < 16 ? ROWS : 16;
+template <int ROWS>
+constexpr int kJoinThreads = 8 * kJoinRows<ROWS>;
+
 template <int D, class U>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
+__global__ void __launch_bounds__(kJoinThreads<U::R>) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
 {
-    const int r16 = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
-    const int h = bh % a.c.heads, b = bh / a.c.heads, rt = r16 / (U::R / 16), sub = r16 % (U::R / 16) * 16;
+    constexpr int JR = kJoinRows<U::R>;
+    const int jr = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
+    const int h = bh % a.c.heads, b = bh / a.c.heads, rt = jr / (U::R / JR), sub = jr % (U::R / JR) * JR;
     const SeqLen s = seq_len(a, b);
-    if (r16 * 16 >= s.m * a.G) return;
+    if (jr * JR >= s.m * a.G) return;
     const uint32_t tiles = U::tiles(a, s, rt), W = a.prefix[a.B];
     const uint32_t w0 = a.prefix[b] + U::before(a, s, h, rt), w1 = w0 + tiles;
     // the share that holds share unit w: the smallest c with w < floor((c + 1) W / shares)

@@ -25,7 +25,6 @@ namespace {
 constexpr int kThreadsP = 512;
 constexpr int kTok = 128;     // slots of a tile
 constexpr int kStep = 64;     // slots of one step of the softmax: a row tile has two buffers of scores
-constexpr int kPoly = 1, kPolyOf = 2;  // pairs of exponentials on the multiply-add pipe, of so many
 constexpr int kScaleRing = 4;  // tiles whose key scales are kept: the converter is at most two ahead
 
 // units of 256 rows; a unit's tiles end with the last slot that any of its rows sees
@@ -103,24 +102,6 @@ __device__ __forceinline__ void put_codes(unsigned char* run, int row, int c, ui
         }
     *reinterpret_cast<uint4*>(run + swz(row, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4*>(run + swz(row, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-}
-
-// 2^x of a pair on the multiply-add pipe (the exponential unit gives 16 results a cycle and would bound
-// the softmax): x = n + f with n the nearest integer, 2^f by its degree-4 minimax polynomial on
-// [-1/2, 1/2] (relative error 2.6e-6), n added to the exponent.  x up to 126; below -126: 2^-126.
-__device__ __forceinline__ float2 exp2_poly(float2 x)
-{
-    const float magic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are n, the rest vanishes in the shift below
-    x.x = fmaxf(x.x, -126.0f);
-    x.y = fmaxf(x.y, -126.0f);
-    const float2 t = f2add(x, make_float2(magic, magic));
-    const float2 f = f2sub(x, f2sub(t, make_float2(magic, magic)));
-    float2 p = __ffma2_rn(f, make_float2(0.00957010128f, 0.00957010128f), make_float2(0.0559178591f, 0.0559178591f));
-    p = __ffma2_rn(p, f, make_float2(0.240247443f, 0.240247443f));
-    p = __ffma2_rn(p, f, make_float2(0.693121791f, 0.693121791f));
-    p = __ffma2_rn(p, f, make_float2(0.999999285f, 0.999999285f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
 template <int D>
@@ -272,8 +253,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                             const float cq = cg[2 * p + (y >> 3)];
                             float2 e = __ffma2_rn(make_float2(__uint_as_float(S[p][2 * y]), __uint_as_float(S[p][2 * y + 1])),
                                                   make_float2(cq, cq), nsub);
-                            if (y % kPolyOf < kPoly) e = exp2_poly(e);
-                            else e = make_float2(ex2(e.x), ex2(e.y));
+                            e = make_float2(ex2(e.x), ex2(e.y));
                             sum = f2add(sum, e);
                             P[y] = pack_f16(e.x, e.y);
                         }
@@ -285,7 +265,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_ready[t][buf]);
                 }
-                if (m == -INFINITY) l = 0.0f;  // no slot seen: not even the polynomial's smallest value
                 // the segment's accumulator
                 wait(&sm.o_full[t], seg_n);
                 if (alive) {
@@ -519,7 +498,7 @@ cudaError_t launch_many(const AttendArgs& a, int grid, cudaStream_t st)
     kv8_prefill_kernel<D><<<grid, kThreadsP, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rts = (a.Sq * a.G + 15) / 16;
-    kv8_join_kernel<D, ManyRows><<<(unsigned)(a.B * a.c.heads * rts), 128, 0, st>>>(a, rts, grid);
+    kv8_join_kernel<D, ManyRows><<<(unsigned)(a.B * a.c.heads * rts), kJoinThreads<kManyRows>, 0, st>>>(a, rts, grid);
     return cudaGetLastError();
 }
 
