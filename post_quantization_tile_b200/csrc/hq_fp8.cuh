@@ -32,6 +32,30 @@ __device__ __forceinline__ void slot_write(WsHeader* ws, uint32_t slots, uint32_
 }
 
 // ------------------------------------------------------------------------------------------------
+// Kernels of one call that follow one another: the first lets the second's blocks come up while it
+// still runs (after_me), the second waits for its results before it touches them (wait_before_me).
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void after_me() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_before_me() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// launches a kernel that starts with wait_before_me()
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// ------------------------------------------------------------------------------------------------
 // e4m3
 // ------------------------------------------------------------------------------------------------
 // two binary32 -> two e4m3 codes (lo in the low byte), nearest even, saturating at 448

@@ -8,8 +8,8 @@ namespace hq {
 namespace {
 
 // ------------------------------------------------------------------------------------------------
-// Append.  A page's scale is the largest that any of its tokens asked for.  One thread block takes one
-// (sequence, head, page that new tokens touch) of keys or values: it reads the new rows once into
+// Append.  A page's scale is the largest that any of its tokens asked for.  One thread block takes the keys
+// and values of one (sequence, head, page that new tokens touch): it reads the new rows once into
 // registers, reduces their maximum, joins it with the page's scale if the page held tokens before,
 // codes the new rows and, only where the scale grew, the older rows again (exact in e4m3 but for
 // codes that become subnormal).  Bound by the rows read and the codes written; a step of one token
@@ -26,7 +26,7 @@ struct AppendArgs {
     int64_t table_stride, max_pages;
     const int32_t* lens;
     const int32_t* n_new;
-    uint32_t span, units;  // pages a sequence's new tokens can touch; 2 * B * heads * span
+    uint32_t span, units;  // pages a sequence's new tokens can touch; B * heads * span
     WsHeader* ws;
 };
 
@@ -36,17 +36,16 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
 {
     constexpr int LPR = D / 8;                // lanes of one row
     constexpr int RPP = kAThreads / LPR;      // rows of one pass
-    __shared__ uint32_t warp_max[kAThreads / 32];
+    __shared__ uint32_t warp_max[2][kAThreads / 32];
     __shared__ uint32_t s_status, s_nonfinite;
     const int sub = threadIdx.x % LPR, row = threadIdx.x / LPR;
     if (threadIdx.x == 0) s_status = 0u, s_nonfinite = 0u;
     __syncthreads();
     const int page = a.c.page;
     for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x) {
-        const uint32_t rest = u / a.span, sp = u - rest * a.span;
-        const int kv = rest & 1;
-        const int b = (int)((rest >> 1) / (uint32_t)a.c.heads), h = (int)((rest >> 1) - (uint32_t)b * a.c.heads);
-        int64_t first = a.lens[b];
+        const uint32_t bh = u / a.span, sp = u - bh * a.span;
+        const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * a.c.heads);
+        const int64_t first = a.lens[b];
         int64_t n = a.n_new ? (int64_t)a.n_new[b] : a.S;
         const bool odd = first < 0 || n < 0 || n > a.S || first + n > a.max_pages * page;
         if (odd && threadIdx.x == 0 && sp == 0) atomicOr(&s_status, kStRange);
@@ -57,55 +56,64 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
         if (at >= a.max_pages || lo64 >= hi64) continue;
         const int lo = (int)(lo64 - at * page), hi = (int)(hi64 - at * page);
         const int32_t id = a.table[b * a.table_stride + at];
+        // the new rows are on their way before the page is known
+        Raw8<T> v[2][PASSES];
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const T* x = static_cast<const T*>(a.x[kv]) + b * a.sb[kv] + h * a.sh[kv] + (at * page - first) * a.ss[kv];
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int r = p * RPP + row;
+                v[kv][p].zero();
+                if (r >= lo && r < hi) v[kv][p].load(x + r * a.ss[kv] + sub * 8);
+            }
+        }
         if (id < 0 || id >= a.c.pages) {
             if (threadIdx.x == 0) atomicOr(&s_status, kStRange);
             continue;
         }
-        const T* x = static_cast<const T*>(a.x[kv]) + b * a.sb[kv] + h * a.sh[kv] + (at * page - first) * a.ss[kv];
         const int64_t ph = (int64_t)id * a.c.heads + h;
-        uint8_t* codes = (kv ? a.c.v : a.c.k) + ph * page * D;
-        float* scale = (kv ? a.c.v_scale : a.c.k_scale) + ph;
-        const float s_old = lo > 0 ? *scale : 0.0f;
-        Raw8<T> v[PASSES];
-        uint32_t top = 0;
+        const float s_old[2] = {lo > 0 ? a.c.k_scale[ph] : 0.0f, lo > 0 ? a.c.v_scale[ph] : 0.0f};
+        uint32_t top[2] = {0u, 0u};
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int r = p * RPP + row;
-            v[p].zero();
-            if (r >= lo && r < hi) v[p].load(x + r * a.ss[kv] + sub * 8);
-        }
+        for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            uint32_t m = v[p].amax_bits();
+            for (int p = 0; p < PASSES; ++p) {
+                uint32_t m = v[kv][p].amax_bits();
 #pragma unroll
-            for (int o = LPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            if (m > kFiniteMax) {  // a token with NaN or infinity is kept as zeros
-                v[p].zero();
-                if (sub == 0) atomicOr(&s_status, kStNonfinite), atomicAdd(&s_nonfinite, 1u);
-                m = 0;
+                for (int o = LPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                if (m > kFiniteMax) {  // a token with NaN or infinity is kept as zeros
+                    v[kv][p].zero();
+                    if (sub == 0) atomicOr(&s_status, kStNonfinite), atomicAdd(&s_nonfinite, 1u);
+                    m = 0;
+                }
+                top[kv] = max(top[kv], m);
             }
-            top = max(top, m);
+            top[kv] = __reduce_max_sync(0xFFFFFFFFu, top[kv]);
+            if ((threadIdx.x & 31) == 0) warp_max[kv][threadIdx.x >> 5] = top[kv];
         }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
-        __syncthreads();  // also: every thread has read the old scale
+        __syncthreads();  // also: every thread has read the old scales
 #pragma unroll
-        for (int w = 0; w < kAThreads / 32; ++w) top = max(top, warp_max[w]);
-        if (top > kAmaxLimit && threadIdx.x == 0) atomicOr(&s_status, kStRange);
-        const float s_new = fmaxf(s_old, exp2_int(scale_exp(top)));
-        if (threadIdx.x == 0 && s_new != s_old) *scale = s_new;
-        const float inv = __fdiv_rn(1.0f, s_new);
-        const bool grown = lo > 0 && s_new != s_old;
-        const float ratio = __fdiv_rn(s_old, s_new);
+        for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int r = p * RPP + row;
-            uint2* q = reinterpret_cast<uint2*>(codes + r * D + sub * 8);
-            if (r >= lo && r < hi) {
-                *q = encode8(v[p], inv);
-            } else if (grown && r < lo) {
-                const uint2 w = *q;
-                *q = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
+            for (int w = 0; w < kAThreads / 32; ++w) top[kv] = max(top[kv], warp_max[kv][w]);
+            if (top[kv] > kAmaxLimit && threadIdx.x == 0) atomicOr(&s_status, kStRange);
+            const float s_new = fmaxf(s_old[kv], exp2_int(scale_exp(top[kv])));
+            if (threadIdx.x == 0 && s_new != s_old[kv]) (kv ? a.c.v_scale : a.c.k_scale)[ph] = s_new;
+            uint8_t* codes = (kv ? a.c.v : a.c.k) + ph * page * D + sub * 8;
+            const float inv = __fdiv_rn(1.0f, s_new);
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int r = p * RPP + row;
+                if (r >= lo && r < hi) *reinterpret_cast<uint2*>(codes + r * D) = encode8(v[kv][p], inv);
+            }
+            if (lo > 0 && s_new != s_old[kv]) {
+                const float ratio = __fdiv_rn(s_old[kv], s_new);
+                for (int r = row; r < lo; r += RPP) {
+                    uint2* q = reinterpret_cast<uint2*>(codes + r * D);
+                    const uint2 w = *q;
+                    *q = make_uint2(rescale4(w.x, ratio), rescale4(w.y, ratio));
+                }
             }
         }
         __syncthreads();  // warp_max is written again by the next unit
@@ -139,7 +147,7 @@ struct EvictArgs {
     int32_t* out_lens;
     float* out_w;
     int64_t ob, oh;
-    int32_t* idx;  // [B * heads, budget] kept slots
+    int32_t* idx;  // [B * heads, budget] cache rows of the kept slots, -1 on a page outside the pool
     uint32_t to_pages, units;
     int page_shift, keys;
     WsHeader* ws;
@@ -200,9 +208,15 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
     const float* w = a.w + b * a.wb + h * a.wh;
     float* out_w = a.out_w ? a.out_w + b * a.ob + h * a.oh : nullptr;
     int32_t* idx = a.idx + (int64_t)blockIdx.x * a.budget;
+    const int32_t* table = a.table + b * a.table_stride;
+    auto row_of = [&](int slot) {
+        const int32_t id = __ldg(table + (slot >> a.page_shift));
+        return id >= 0 && id < a.c.pages ? (int)(((uint32_t)id * a.c.heads + h) << a.page_shift) + (slot & (a.c.page - 1)) : -1;
+    };
+    after_me();
     if (n <= a.budget) {
         for (int i = threadIdx.x; i < n; i += kEThreads) {
-            idx[i] = i;
+            idx[i] = row_of(i);
             if (out_w) out_w[i] = w[i];
         }
         return;
@@ -259,35 +273,35 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
             const uint32_t k = key_at(i);
             if (k > key || (k == key && at < need)) {
                 const uint32_t pos = above + min(at, need);
-                idx[pos] = i;
+                idx[pos] = row_of(i);
                 if (out_w) out_w[pos] = w[i];
             }
             above += k > key;
             at += k == key;
         }
     for (int i = threadIdx.x; i < recent; i += kEThreads) {
-        idx[keep - recent + i] = old + i;
+        idx[keep - recent + i] = row_of(old + i);
         if (out_w) out_w[keep - recent + i] = w[old + i];
     }
 }
 
-// Second step: one thread block per (sequence, head, new page) gathers its rows of keys and of values.  A
-// page's scale is the largest of its rows' old scales; a row with a smaller one is coded again.  The
-// rows' places and scales are looked up once, by one thread each; then every thread has all its
-// 16-byte loads under way before the first is stored.  Bound by the scattered 64- or 128-byte rows.
+// Second step: one thread block per (sequence, head, new page) gathers its rows of keys and values.  A page's
+// scale is the largest of its rows' old scales; a row with a smaller one is coded again.  Every thread
+// has all its 16-byte loads under way, beside the scales', before the first is stored.  Bound by the
+// scattered 64- or 128-byte rows.
 constexpr int kMThreads = 256;
 
 template <int D, int PASSES>
 __global__ void __launch_bounds__(kMThreads) kv8_move_kernel(const EvictArgs a)
 {
     constexpr int LPR = D / 16, RPP = kMThreads / LPR;
-    __shared__ int64_t s_row[128];
     __shared__ float s_ks[128], s_vs[128];
     __shared__ uint32_t s_top[2], s_status;
     const int page = a.c.page;
     const int sub = threadIdx.x % LPR, row = threadIdx.x / LPR;
     if (threadIdx.x == 0) s_status = 0u, s_top[0] = 0u, s_top[1] = 0u;
     __syncthreads();
+    wait_before_me();  // the kept rows
     for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x) {
         const uint32_t bh = u / a.to_pages, pg = u - bh * a.to_pages;
         const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * a.c.heads);
@@ -299,43 +313,35 @@ __global__ void __launch_bounds__(kMThreads) kv8_move_kernel(const EvictArgs a)
         const int rows = (int)min((int64_t)page, n - (int64_t)pg * page);
         if (rows <= 0) continue;
         const int32_t id = a.to[b * a.to_stride + pg];
-        bool bad = id < 0 || id >= a.c.pages;
-        uint32_t ktop = 0, vtop = 0;  // positive floats order like their bit patterns
-        if ((int)threadIdx.x < rows) {
-            const int32_t slot = a.idx[(int64_t)bh * a.budget + (int64_t)pg * page + threadIdx.x];
-            const int32_t from = a.table[b * a.table_stride + (slot >> a.page_shift)];
-            if (from < 0 || from >= a.c.pages) {
-                bad = true;
-            } else {
-                const int64_t ph = (int64_t)from * a.c.heads + h;
-                const float ks = a.c.k_scale[ph], vs = a.c.v_scale[ph];
-                s_row[threadIdx.x] = (ph << a.page_shift) + (slot & (page - 1));
-                s_ks[threadIdx.x] = ks;
-                s_vs[threadIdx.x] = vs;
-                ktop = __float_as_uint(ks);
-                vtop = __float_as_uint(vs);
+        const int32_t* from = a.idx + (int64_t)bh * a.budget + (int64_t)pg * page;
+        const int mine = (int)threadIdx.x < rows ? from[threadIdx.x] : 0;
+        uint4 q[2][PASSES];
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int r = p * RPP + row, at = r < rows ? from[r] : -1;
+            if (at >= 0) {
+                q[0][p] = *reinterpret_cast<const uint4*>(a.c.k + (int64_t)at * D + sub * 16);
+                q[1][p] = *reinterpret_cast<const uint4*>(a.c.v + (int64_t)at * D + sub * 16);
             }
+        }
+        uint32_t ktop = 0, vtop = 0;  // positive floats order like their bit patterns
+        if ((int)threadIdx.x < rows && mine >= 0) {
+            const float ks = a.c.k_scale[mine >> a.page_shift], vs = a.c.v_scale[mine >> a.page_shift];
+            s_ks[threadIdx.x] = ks;
+            s_vs[threadIdx.x] = vs;
+            ktop = __float_as_uint(ks);
+            vtop = __float_as_uint(vs);
         }
         ktop = __reduce_max_sync(0xFFFFFFFFu, ktop);
         vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
         if ((threadIdx.x & 31) == 0 && (ktop | vtop)) atomicMax(&s_top[0], ktop), atomicMax(&s_top[1], vtop);
-        if (__syncthreads_or(bad)) {  // a page outside the pool: this page is left as it was
+        if (__syncthreads_or(mine < 0 || id < 0 || id >= a.c.pages)) {  // a page outside the pool: left as it was
             if (threadIdx.x == 0) atomicOr(&s_status, kStRange), s_top[0] = 0u, s_top[1] = 0u;
             __syncthreads();
             continue;
         }
         const float kto = __uint_as_float(s_top[0]), vto = __uint_as_float(s_top[1]);
         const int64_t to = (int64_t)id * a.c.heads + h;
-        uint4 q[2][PASSES];
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int r = p * RPP + row;
-            if (r < rows) {
-                const int64_t at = s_row[r] * D + sub * 16;
-                q[0][p] = *reinterpret_cast<const uint4*>(a.c.k + at);
-                q[1][p] = *reinterpret_cast<const uint4*>(a.c.v + at);
-            }
-        }
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
             const int r = p * RPP + row;
@@ -343,10 +349,12 @@ __global__ void __launch_bounds__(kMThreads) kv8_move_kernel(const EvictArgs a)
                 const int64_t at = ((to << a.page_shift) + r) * D + sub * 16;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const float ratio = __fdiv_rn(kv ? s_vs[r] : s_ks[r], kv ? vto : kto);
+                    const float s = kv ? s_vs[r] : s_ks[r], t = kv ? vto : kto;
                     uint4 x = q[kv][p];
-                    if (ratio != 1.0f)
+                    if (s != t) {
+                        const float ratio = __fdiv_rn(s, t);
                         x = make_uint4(rescale4(x.x, ratio), rescale4(x.y, ratio), rescale4(x.z, ratio), rescale4(x.w, ratio));
+                    }
                     *reinterpret_cast<uint4*>((kv ? a.c.v : a.c.k) + at) = x;
                 }
             }
@@ -361,13 +369,13 @@ __global__ void __launch_bounds__(kMThreads) kv8_move_kernel(const EvictArgs a)
 }
 
 template <int D>
-void launch_move(const EvictArgs& a, int grid, cudaStream_t st)
+cudaError_t launch_move(const EvictArgs& a, int grid, cudaStream_t st)
 {
     constexpr int RPP = kMThreads / (D / 16);
     const int passes = (a.c.page + RPP - 1) / RPP;
-    if (passes == 1) kv8_move_kernel<D, 1><<<grid, kMThreads, 0, st>>>(a);
-    else if (passes == 2) kv8_move_kernel<D, 2><<<grid, kMThreads, 0, st>>>(a);
-    else kv8_move_kernel<D, 128 / RPP><<<grid, kMThreads, 0, st>>>(a);
+    if (passes == 1) return launch_after(kv8_move_kernel<D, 1>, dim3((unsigned)grid), kMThreads, 0, st, a);
+    if (passes == 2) return launch_after(kv8_move_kernel<D, 2>, dim3((unsigned)grid), kMThreads, 0, st, a);
+    return launch_after(kv8_move_kernel<D, 128 / RPP>, dim3((unsigned)grid), kMThreads, 0, st, a);
 }
 
 template <typename T, int D>
@@ -427,9 +435,9 @@ extern "C" hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t 
     a.lens = p->lens;
     a.n_new = p->n_new;
     const int64_t span = (p->S + p->cache.page - 2) / p->cache.page + 1;
-    if (span > (((int64_t)1 << 31) - 1) / (2 * p->cache.heads) / p->B) return HQ_ERR_UNSUPPORTED;
+    if (span > (((int64_t)1 << 31) - 1) / p->cache.heads / p->B) return HQ_ERR_UNSUPPORTED;
     a.span = (uint32_t)span;
-    a.units = (uint32_t)(2 * p->B * p->cache.heads * span);
+    a.units = (uint32_t)(p->B * p->cache.heads * span);
     a.ws = static_cast<WsHeader*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int grid = slots_grid(a.units);
@@ -484,6 +492,7 @@ extern "C" hq_status_t hq_kv8_evict(const hq_kv8_evict_t* p, void* ws, size_t ws
     a.oh = p->ow_stride[1];
     a.idx = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + kSlotBytes);
     if (p->B * p->cache.heads > (((int64_t)1 << 31) - 1) / to_pages) return HQ_ERR_UNSUPPORTED;
+    if (p->cache.pages * p->cache.heads > (((int64_t)1 << 31) - 1) / page) return HQ_ERR_UNSUPPORTED;  // cache rows in 31 bits
     a.to_pages = (uint32_t)to_pages;
     a.units = (uint32_t)(p->B * p->cache.heads * to_pages);
     a.page_shift = page_shift_of(p->cache.page);
@@ -496,7 +505,6 @@ extern "C" hq_status_t hq_kv8_evict(const hq_kv8_evict_t* p, void* ws, size_t ws
     kv8_select_kernel<<<(unsigned)(p->B * p->cache.heads), kEThreads, 4 * (size_t)a.keys, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return HQ_ERR_CUDA;
     const int grid = slots_grid(a.units);
-    if (p->cache.dim == 64) launch_move<64>(a, grid, st);
-    else launch_move<128>(a, grid, st);
-    return cudaGetLastError() == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+    const cudaError_t e = p->cache.dim == 64 ? launch_move<64>(a, grid, st) : launch_move<128>(a, grid, st);
+    return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }

@@ -261,8 +261,9 @@ __global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
         fence_mbar_init();
     }
     if (share_prefix<U, kThreadsA>(a, pre, sm.scan) && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
+    after_me();
     const uint32_t W = pre[a.B];
-    const uint32_t shares = min(W, gridDim.x);  // none is empty: the join walks a unit's shares one by one
+    const uint32_t shares = share_count(W, gridDim.x);
     uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
     const uint32_t w1 = blockIdx.x < shares ? (uint32_t)((uint64_t)(blockIdx.x + 1) * W / shares) : 0u;
     uint32_t status = 0u;
@@ -472,12 +473,16 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
     const SeqLen s = seq_len(a, b);
     const int n = (int)min((int64_t)s.n, a.L);
     const int tok = (blockIdx.x * kWarps + warp) * 16;
-    if (tok >= n) return;
+    if (tok >= n) {
+        wait_before_me();  // in every block, so that this grid never ends before those it follows
+        return;
+    }
     const int row = locate(a, a.table + b * a.table_stride, h, tok);
     const bool ok = row >= 0;
     KeyGroup<D> k;
     k.load_global(a.c.k + (int64_t)(ok ? row : 0) * D, ok);
     const float ks = ok ? __ldg(a.c.k_scale + (row >> a.page_shift)) : 0.0f;
+    wait_before_me();  // the rows' sums
     float sum[2] = {0.0f, 0.0f};
     const float* lse2 = a.lse2 + ((int64_t)b * a.c.heads + h) * a.G * a.Sq;
     const int rows = s.m * a.G;
@@ -541,8 +546,7 @@ cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
     kv8_attend_kernel<D, ROWS><<<grid, kThreadsA, smem, st>>>(a, tk, tv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rts = (a.Sq * a.G + ROWS - 1) / ROWS;
-    kv8_join_kernel<D, FewRows<ROWS>><<<(unsigned)(a.B * a.c.heads * rts), kJoinThreads<ROWS>, 0, st>>>(a, rts, grid);
-    return cudaGetLastError();
+    return launch_after(kv8_join_kernel<D, FewRows<ROWS>>, dim3((unsigned)(a.B * a.c.heads * rts)), kJoinThreads<D, ROWS>, 0, st, a, rts, grid);
 }
 
 template <int D>
@@ -555,8 +559,7 @@ cudaError_t launch_attend(const AttendArgs& a, bool many, cudaStream_t st)
     if (a.w) {
         const int64_t most = a.slots < a.L ? a.slots : a.L;
         const dim3 wg((unsigned)((most + 16 * kWarps - 1) / (16 * kWarps)), (unsigned)a.c.heads, (unsigned)a.B);
-        kv8_weights_kernel<D><<<wg, kThreadsA, 0, st>>>(a);
-        e = cudaGetLastError();
+        e = launch_after(kv8_weights_kernel<D>, wg, kThreadsA, 0, st, a);
     }
     return e;
 }

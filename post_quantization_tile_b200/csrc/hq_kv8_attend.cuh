@@ -134,6 +134,15 @@ __device__ __forceinline__ bool share_prefix(const AttendArgs& a, uint32_t* pre,
     return odd;
 }
 
+// Shares of W tiles over `grid` thread blocks: none is empty (the join walks a unit's shares one by one),
+// and none is so short that joining costs more than it saves.
+constexpr uint32_t kShareTiles = 2;
+__host__ __device__ __forceinline__ uint32_t share_count(uint32_t W, uint32_t grid)
+{
+    const uint32_t most = (W + kShareTiles - 1) / kShareTiles;
+    return most < grid ? most : grid;
+}
+
 // the part of a thread block's share [w0, w1) that lies in the unit of tile w0
 struct Segment {
     int b, h, rt;
@@ -156,58 +165,63 @@ __device__ __forceinline__ Segment segment_at(const AttendArgs& a, const uint32_
     return g;
 }
 
-// Joins the parts of the units that were cut, up to sixteen rows a thread block, eight threads a row, and
-// writes zeros where a row sees nothing.  U: how the attention kernel makes units (U::R rows each) and
-// lays them end to end.
+// Joins the parts of the units that were cut, up to sixteen rows a thread block, and writes zeros where a
+// row sees nothing.  A row's threads take four dims each; first they find the row's reference
+// together.  U: how the attention kernel makes units (U::R rows each) and lays them end to end.
 template <int ROWS>
 constexpr int kJoinRows = ROWS < 16 ? ROWS : 16;
-template <int ROWS>
-constexpr int kJoinThreads = 8 * kJoinRows<ROWS>;
+template <int D, int ROWS>
+constexpr int kJoinThreads = D / 4 * kJoinRows<ROWS>;
 
 template <int D, class U>
-__global__ void __launch_bounds__(kJoinThreads<U::R>) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
+__global__ void __launch_bounds__((kJoinThreads<D, U::R>)) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
 {
-    constexpr int JR = kJoinRows<U::R>;
+    constexpr int JR = kJoinRows<U::R>, TPR = D / 4;
     const int jr = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
     const int h = bh % a.c.heads, b = bh / a.c.heads, rt = jr / (U::R / JR), sub = jr % (U::R / JR) * JR;
     const SeqLen s = seq_len(a, b);
-    if (jr * JR >= s.m * a.G) return;
-    const uint32_t tiles = U::tiles(a, s, rt), W = a.prefix[a.B];
-    const uint32_t w0 = a.prefix[b] + U::before(a, s, h, rt), w1 = w0 + tiles;
-    // the share that holds share unit w: the smallest c with w < floor((c + 1) W / shares)
-    const uint32_t shares = min(W, (uint32_t)grid);
-    const int c0 = tiles ? (int)(((uint64_t)(w0 + 1) * shares - 1) / W) : 0;
-    const int c1 = tiles ? (int)(((uint64_t)w1 * shares - 1) / W) : 0;
-    if (tiles && c0 == c1) return;  // whole: written already
-    constexpr int TPR = 8, DPT = D / TPR;
-    const int r = sub + threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * DPT, rr = rt * U::R + r;
-    if (rr >= s.m * a.G) return;
-    float M = -INFINITY, L = 0.0f, y[DPT];
-#pragma unroll
-    for (int d = 0; d < DPT; ++d) y[d] = 0.0f;
-    if (tiles) {
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(2 * c + (c == c0)) * U::R + r].x);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t at = (int64_t)(2 * c + (c == c0)) * U::R + r;
-            const float2 ml = a.part_ml[at];
-            const float f = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
-            L = fmaf(ml.y, f, L);
-#pragma unroll
-            for (int d = 0; d < DPT; d += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + d0 + d);
-                y[d] = fmaf(x.x, f, y[d]), y[d + 1] = fmaf(x.y, f, y[d + 1]), y[d + 2] = fmaf(x.z, f, y[d + 2]), y[d + 3] = fmaf(x.w, f, y[d + 3]);
-            }
-        }
+    const bool rows = jr * JR < s.m * a.G;
+    __shared__ uint32_t s_tiles, s_before;
+    if (threadIdx.x == 0 && rows) {  // sums over row tiles: one thread's work
+        s_tiles = U::tiles(a, s, rt);
+        s_before = U::before(a, s, h, rt);
     }
-    if (d0 == 0) write_lse(a, b, h, rr, M, L);
+    __syncthreads();
+    const uint32_t tiles = s_tiles, before = s_before;
+    after_me();
+    wait_before_me();  // in every block, so that this grid never ends before the one it joins
+    if (!rows) return;
+    const uint32_t W = a.prefix[a.B], w0 = a.prefix[b] + before, w1 = w0 + tiles;
+    // the share that holds tile w: the smallest c with w < floor((c + 1) W / shares)
+    const uint32_t shares = share_count(W, (uint32_t)grid);
+    const int c0 = tiles ? (int)(((uint64_t)(w0 + 1) * shares - 1) / W) : 0;
+    const int c1 = tiles ? (int)(((uint64_t)w1 * shares - 1) / W) : -1;
+    if (tiles && c0 == c1) return;  // whole: written already
+    const int r = sub + threadIdx.x / TPR, lane = threadIdx.x % TPR, rr = rt * U::R + r;
+    if (rr >= s.m * a.G) return;  // a row's threads are whole halves of warps: the shuffles below stay inside
+    const uint32_t mask = TPR == 32 ? 0xFFFFFFFFu : 0xFFFFu << (threadIdx.x & 16);
+    auto at = [&](int c) { return (int64_t)(2 * c + (c == c0)) * U::R + r; };
+    float M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += TPR) M = fmaxf(M, a.part_ml[at(c)].x);
+#pragma unroll
+    for (int o = TPR / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(mask, M, o));
+    float L = 0.0f;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int c = c0; c <= c1; ++c) {
+        const float2 ml = a.part_ml[at(c)];
+        const float4 x = *reinterpret_cast<const float4*>(a.part_o + at(c) * D + 4 * lane);
+        const float f = ml.x == -INFINITY ? 1.0f : ex2(ml.x - M);
+        L = fmaf(ml.y, f, L);
+        y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
+    }
+    if (lane == 0) write_lse(a, b, h, rr, M, L);
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     int head, i;
     row_place(a, h, rr, head, i);
-    __nv_bfloat16* out = a.out + b * a.ob + head * a.oh + (int64_t)i * a.os + d0;
-#pragma unroll
-    for (int d = 0; d < DPT; d += 2) *reinterpret_cast<__nv_bfloat162*>(out + d) = __floats2bfloat162_rn(y[d] * inv, y[d + 1] * inv);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * inv, y.y * inv), hi = __floats2bfloat162_rn(y.z * inv, y.w * inv);
+    *reinterpret_cast<uint2*>(a.out + b * a.ob + head * a.oh + (int64_t)i * a.os + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 // what the attention entry point needs of the kernel for many rows (hq_kv8_prefill.cu)

@@ -135,9 +135,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
     const bool odd_len = share_prefix<ManyRows, kThreadsP>(a, pre, sm.scan);  // two block barriers
     tc_fence_after();
     if (odd_len && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
+    after_me();
     const uint32_t tbase = sm.tmem_base;
     const uint32_t W = pre[a.B];
-    const uint32_t shares = min(W, gridDim.x);  // none is empty: the join walks a unit's shares one by one
+    const uint32_t shares = share_count(W, gridDim.x);
     uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
     const uint32_t w1 = blockIdx.x < shares ? (uint32_t)((uint64_t)(blockIdx.x + 1) * W / shares) : 0u;
     // After a wait that ran out a warp only walks its loops, without waiting or working.
@@ -498,8 +499,7 @@ cudaError_t launch_many(const AttendArgs& a, int grid, cudaStream_t st)
     kv8_prefill_kernel<D><<<grid, kThreadsP, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rts = (a.Sq * a.G + 15) / 16;
-    kv8_join_kernel<D, ManyRows><<<(unsigned)(a.B * a.c.heads * rts), kJoinThreads<kManyRows>, 0, st>>>(a, rts, grid);
-    return cudaGetLastError();
+    return launch_after(kv8_join_kernel<D, ManyRows>, dim3((unsigned)(a.B * a.c.heads * rts)), kJoinThreads<D, kManyRows>, 0, st, a, rts, grid);
 }
 
 }  // namespace
