@@ -449,6 +449,218 @@ cudaError_t launch_gemm_fp8_pair(const F8Args& a, const CUtensorMap& ta, const C
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------------------------------------
+// The same product for few rows of A (M <= 64): bound by the bytes of W, which want many loads under way
+// on every SM from the first moment.  The weights take the MMA's 128 rows and A's rows its NT columns
+// (16, 32 or 64), and a cluster of up to eight CTAs divides the blocks of one 128-row slab of W, so that
+// a 4096 x 4096 weight is one ring fill on 128 SMs.  Each CTA's scaled sums (binary32) meet over
+// distributed shared memory: CTA c of the cluster adds, in the order of the ranks, the columns
+// c NT / size .. of all of them and stores those.
+// ------------------------------------------------------------------------------------------------
+template <int NT>
+struct FewCfg {
+    static constexpr int STAGES = NT == 64 ? 7 : 8;
+    static constexpr int ACC = 256 / NT;  // accumulator slots in 256 TMEM columns
+};
+constexpr int kFewThreads = 192;  // producer, MMA issue, four epilogue warps
+
+template <int NT>
+struct FewSmem {
+    using C = FewCfg<NT>;
+    alignas(1024) uint8_t w[C::STAGES][GM * GK];
+    alignas(1024) uint8_t a[C::STAGES][NT * GK];
+    alignas(16) float red[NT * GM];      // [source rank][column of this CTA's share][row of W]
+    alignas(16) float factor[4][2][NT];  // of a block's columns, by epilogue warp and parity
+    alignas(8) uint64_t full[C::STAGES];
+    uint64_t empty[C::STAGES];
+    uint64_t acc_full[C::ACC];
+    uint64_t acc_empty[C::ACC];
+    uint32_t tmem_base;
+    uint32_t status;
+};
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, float x)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    gemm_fp8_few_kernel(const F8Args a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tW, int parts)
+{
+    using C = FewCfg<NT>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    FewSmem<NT>& sm = *reinterpret_cast<FewSmem<NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int KB = (int)((a.K + GK - 1) / GK);
+    const int k0 = (int)((int64_t)KB * rank / parts), k1 = (int)((int64_t)KB * (rank + 1) / parts);
+    const int n0 = (int)(blockIdx.x / (uint32_t)parts) * GM;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int s = 0; s < C::ACC; ++s) {
+            mbar_init(&sm.acc_full[s], 1);
+            mbar_init(&sm.acc_empty[s], 4);
+        }
+        sm.status = 0u;
+        fence_mbar_init();
+        // the first loads need none of the other warps
+        for (int kb = k0; kb < k1 && kb < k0 + C::STAGES; ++kb) {
+            const int s = kb - k0;
+            mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(GM * GK + NT * GK));
+            tma_load_2d(sm.w[s], &tW, kb * GK, n0, &sm.full[s]);
+            tma_load_2d(sm.a[s], &tA, kb * GK, 0, &sm.full[s]);
+        }
+    }
+    if (warp == 1) tmem_alloc(&sm.tmem_base, 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = sm.tmem_base;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool alive = true;
+            for (int kb = k0 + C::STAGES; alive && kb < k1; ++kb) {
+                const int it = kb - k0, s = it % C::STAGES;
+                if (!mbar_wait_sleep(&sm.empty[s], (uint32_t)((it / C::STAGES - 1) & 1))) {
+                    atomicOr(&sm.status, kStTimeout);
+                    alive = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(GM * GK + NT * GK));
+                tma_load_2d(sm.w[s], &tW, kb * GK, n0, &sm.full[s]);
+                tma_load_2d(sm.a[s], &tA, kb * GK, 0, &sm.full[s]);
+            }
+            // no copy may be in flight when the block leaves: wait for the last boxes
+            if (alive)
+                for (int it = k1 - k0 > C::STAGES ? k1 - k0 - C::STAGES : 0; it < k1 - k0; ++it)
+                    mbar_wait_sleep(&sm.full[it % C::STAGES], (uint32_t)((it / C::STAGES) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint64_t wd0 = sw128_desc(sm.w[0]), ad0 = sw128_desc(sm.a[0]);
+        const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), leader = elect_lane();
+        for (int it = 0; it < k1 - k0; ++it) {
+            const int s = it % C::STAGES, slot = it % C::ACC;
+            const bool got = (it < C::ACC || mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / C::ACC - 1) & 1))) &&
+                             mbar_wait_sleep(&sm.full[s], (uint32_t)((it / C::STAGES) & 1));
+            if (!__all_sync(0xFFFFFFFFu, got)) {
+                if (lane == 0) atomicOr(&sm.status, kStTimeout);
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < GK / 32; ++kk)
+                mma_f8(tb + (uint32_t)(slot * NT), wd0 + (uint64_t)(s * (GM * GK / 16) + 2 * kk),
+                       ad0 + (uint64_t)(s * (NT * GK / 16) + 2 * kk), idesc_f8(GM, NT), kk > 0 ? 1u : 0u, leader);
+            mma_commit_warp(&sm.empty[s], leader);
+            mma_commit_warp(&sm.acc_full[slot], leader);
+        }
+    }
+    float2 acc[NT / 2];
+    const int q = warp & 3, row = q * 32 + lane;
+    if (warp >= 2) {
+        // one row of W per thread; the columns' factors sa sw go through shared memory, one per lane
+        const int64_t NB = (a.N + 127) / 128;
+        const float* sw = a.sw + n0 / 128;
+#pragma unroll
+        for (int c = 0; c < NT / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
+        constexpr int PER = (NT + 31) / 32;
+        float next[PER];
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int m = lane + 32 * i;
+                next[i] = m < NT && m < a.M && kb < k1 ? __ldg(a.sa + (int64_t)kb * a.M + m) * __ldg(sw + (int64_t)kb * NB) : 0.0f;
+            }
+        };
+        fetch(k0);
+        for (int it = 0; it < k1 - k0; ++it) {
+            const int slot = it % C::ACC;
+            float* factor = sm.factor[q][it & 1];
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < NT) factor[lane + 32 * i] = next[i];
+            fetch(k0 + it + 1);
+            const bool got = mbar_wait_sleep(&sm.acc_full[slot], (uint32_t)((it / C::ACC) & 1));
+            __syncwarp();
+            if (!__all_sync(0xFFFFFFFFu, got)) {
+                if (lane == 0) atomicOr(&sm.status, kStTimeout);
+                break;
+            }
+            tc_fence_after();
+            uint32_t S[NT];
+            tmem_ld_columns<NT>(tbase + ((uint32_t)(q * 32) << 16) + (uint32_t)(slot * NT), S);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.acc_empty[slot]);
+#pragma unroll
+            for (int c = 0; c < NT / 4; ++c) {
+                const float4 f = *reinterpret_cast<const float4*>(factor + 4 * c);
+                acc[2 * c] = __ffma2_rn(make_float2(__uint_as_float(S[4 * c]), __uint_as_float(S[4 * c + 1])), make_float2(f.x, f.y), acc[2 * c]);
+                acc[2 * c + 1] = __ffma2_rn(make_float2(__uint_as_float(S[4 * c + 2]), __uint_as_float(S[4 * c + 3])), make_float2(f.z, f.w),
+                                            acc[2 * c + 1]);
+            }
+        }
+    }
+    // the parts' sums: column c to the CTA that owns it
+    const int share = NT / parts;
+    if (parts > 1) cluster_sync();  // every CTA of the cluster is up (long since)
+    if (warp >= 2) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            const float x = c & 1 ? acc[c / 2].y : acc[c / 2].x;
+            const int owner = c / share;
+            float* to = &sm.red[(rank * share + c - owner * share) * GM + row];
+            if (parts > 1) st_cluster(peer_addr(to, (uint32_t)owner), x);
+            else *to = x;
+        }
+    }
+    tc_fence_before();
+    if (parts > 1) cluster_sync();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tbase, 256);
+    if (warp >= 2 && n0 + row < a.N) {
+        for (int c = 0; c < share; ++c) {
+            const int m = rank * share + c;
+            if (m >= a.M) break;
+            float x = sm.red[c * GM + row];
+            for (int p = 1; p < parts; ++p) x += sm.red[(p * share + c) * GM + row];
+            const int64_t at = (int64_t)m * a.N + n0 + row;
+            if (a.bf16) static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(x);
+            else static_cast<float*>(a.Y)[at] = x;
+        }
+    }
+    if (threadIdx.x == 0) slot_write(a.ws, gridDim.x, blockIdx.x, sm.status, 0u);
+}
+
+template <int NT>
+cudaError_t launch_gemm_fp8_few(const F8Args& a, const CUtensorMap& ta, const CUtensorMap& tw, int parts, cudaStream_t st)
+{
+    const size_t smem = sizeof(FewSmem<NT>) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(gemm_fp8_few_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)((a.N + GM - 1) / GM) * (unsigned)parts);
+    c.blockDim = dim3(kFewThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)parts;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, gemm_fp8_few_kernel<NT>, a, ta, tw, parts);
+}
+
 template <int GN>
 cudaError_t launch_gemm_fp8(const F8Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st)
 {
@@ -479,16 +691,27 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
     if (ws && (ws_bytes < kSlotBytes || (reinterpret_cast<uintptr_t>(ws) & 15u))) return HQ_ERR_ARG;
     DeviceGuard dev(A);
     if (!dev.ok) return HQ_ERR_ARG;
-    const int64_t sms = num_sms(), mt = (M + GM - 1) / GM;
+    const int64_t sms = num_sms(), mt = (M + GM - 1) / GM, kbs = (K + GK - 1) / GK, slabs = (N + GM - 1) / GM;
+    F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, static_cast<WsHeader*>(ws)};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    CUtensorMap ta, tb;
+    if (M <= 64 && slabs <= kMaxSlots / 8) {
+        // as many parts of K as fill the SMs, in powers of two up to a portable cluster
+        int parts = 1;
+        while (parts < 8 && slabs * parts * 2 <= sms && kbs >= parts * 2) parts *= 2;
+        const int nt = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
+        if (!tensor_map_bytes(&ta, A, M, K, lda, nt) || !tensor_map_bytes(&tb, W, N, K, ldw, GM)) return HQ_ERR_CUDA;
+        const cudaError_t e = nt == 16   ? launch_gemm_fp8_few<16>(a, ta, tb, parts, st)
+                              : nt == 32 ? launch_gemm_fp8_few<32>(a, ta, tb, parts, st)
+                                         : launch_gemm_fp8_few<64>(a, ta, tb, parts, st);
+        return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+    }
     const bool pair = ((M + 2 * GM - 1) / (2 * GM)) * ((N + PN - 1) / PN) >= sms / 2;
     int gn = 128;  // the widest tile whose tiles occupy every SM, 32 columns if none does
     while (gn > 32 && mt * ((N + gn - 1) / gn) < sms) gn /= 2;
     // K blocks over all tiles of a CTA are counted in 31 bits
     if ((mt * ((N + gn - 1) / gn) / sms + 1) * ((K + GK - 1) / GK) > ((int64_t)1 << 30)) return HQ_ERR_UNSUPPORTED;
-    CUtensorMap ta, tb;
     if (!tensor_map_bytes(&ta, A, M, K, lda, GM) || !tensor_map_bytes(&tb, W, N, K, ldw, pair ? GM : gn)) return HQ_ERR_CUDA;
-    F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, static_cast<WsHeader*>(ws)};
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = pair        ? launch_gemm_fp8_pair(a, ta, tb, st)
                           : gn == 128 ? launch_gemm_fp8<128>(a, ta, tb, st)
                                     : (gn == 64 ? launch_gemm_fp8<64>(a, ta, tb, st) : launch_gemm_fp8<32>(a, ta, tb, st));

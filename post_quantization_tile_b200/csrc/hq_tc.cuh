@@ -185,6 +185,23 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&v)[3
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+// N consecutive columns (a multiple of 16)
+template <int N>
+__device__ __forceinline__ void tmem_ld_columns(uint32_t taddr, uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 16) tmem_ld16_nowait(taddr + (uint32_t)c, &v[c]);
+}
+
 // registers into 32 consecutive columns of this warp's 32 TMEM lanes; complete after tmem_wait_st()
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
 {

@@ -77,6 +77,10 @@ def codes(hq, g, rows, cols, block):
 @pytest.mark.parametrize("M,N,K_", [(1, 1, 1), (1, 128, 128), (7, 33, 200), (128, 128, 128), (129, 130, 131), (16, 1000, 48),
                                     (300, 257, 1000), (1, 4096, 4096), (130, 5000, 640), (2000, 1300, 300), (2300, 2100, 300), (2300, 2304, 200), (130, 19001, 200)])
 def test_gemm(hq, M, N, K_, dtype):
+    check_gemm(hq, M, N, K_, dtype)
+
+
+def check_gemm(hq, M, N, K_, dtype):
     g = torch.Generator().manual_seed(M + N + K_)
     a, w = codes(hq, g, M, K_, 1), codes(hq, g, N, K_, 128)
     a.scale *= torch.rand(a.scale.shape, generator=g).cuda() + 0.5   # scales need not be powers of two
@@ -107,14 +111,21 @@ def test_gemm_ignores_the_padding_and_writes_in_place(hq):
 
 
 def test_gemm_rows_do_not_depend_on_the_batch(hq):
-    """A row's result is the same whichever rows stand beside it."""
+    """Above 64 rows (where K is not divided) a row's result is the same whichever rows stand beside it."""
     g = torch.Generator().manual_seed(4)
     w = codes(hq, g, 700, 900, 128)
     a = codes(hq, g, 600, 900, 1)
     whole = hq.gemm_fp8(a, w, dtype=torch.float32)
-    for r in (0, 5, 599):
-        one = hq.Fp8Code(1, 900, 1, a.data[r:r + 1].contiguous(), a.scale[:, r:r + 1].contiguous())
-        assert torch.equal(hq.gemm_fp8(one, w, dtype=torch.float32)[0], whole[r])
+    for r in (0, 5, 500):
+        some = hq.Fp8Code(100, 900, 1, a.data[r:r + 100].contiguous(), a.scale[:, r:r + 100].contiguous())
+        assert torch.equal(hq.gemm_fp8(some, w, dtype=torch.float32), whole[r:r + 100])
+
+
+@pytest.mark.parametrize("M", [1, 15, 16, 17, 32, 33, 63, 64, 65])
+@pytest.mark.parametrize("N,K_", [(128, 128), (200, 300), (1000, 2000), (20000, 256), (130, 20000)])
+def test_gemm_few_rows(hq, M, N, K_):
+    """Each width of the kernel for few rows, with K undivided and divided, more blocks than its ring holds."""
+    check_gemm(hq, M, N, K_, torch.float32)
 
 
 def test_graph_replay(hq):
