@@ -592,10 +592,10 @@ def fp8_workspace(nbytes: int = 0, device=None) -> Workspace:
     return Workspace(max(int(nbytes), lib().hq_fp8_workspace_bytes()), device=device)
 
 
-def _scratch(ws: Workspace | None, need: int, dev: torch.device):
+def _scratch(ws: Workspace | None, need: int, dev: int):
     """(pointer, bytes, what keeps it alive) of a call's workspace; need = 0: none unless ws is given."""
     if ws is not None:
-        if ws.buf.device != dev:
+        if ws.buf.get_device() != dev:
             raise ValueError("ws lies on another device")
         return ws.buf.data_ptr(), ws.nbytes, ws
     if not need:
@@ -604,24 +604,27 @@ def _scratch(ws: Workspace | None, need: int, dev: torch.device):
     return buf.data_ptr(), need, buf
 
 
-def _raw_stream(dev: torch.device) -> int:
-    """The current stream of the tensors' device (torch.cuda.current_stream builds an object first)."""
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+# the current stream of a device as a number (torch.cuda.current_stream builds an object first)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(dev: torch.device, t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, contiguous: bool = True) -> int:
-    """data_ptr of a tensor after its checks."""
-    if t.device != dev or t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
+def _on(dev: int, t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, contiguous: bool = True) -> int:
+    """data_ptr of a tensor on CUDA device `dev` after its checks."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{dev}, got {t.dtype} {list(t.shape)} on {t.device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
 def _strides(t: torch.Tensor) -> tuple:
-    """Strides of the leading dimensions; those of length one, which any stride describes, as 0."""
-    n, st = t.shape, t.stride()
-    return tuple([0 if n[i] == 1 else st[i] for i in range(len(n) - 1)])
+    """Strides of a 4-D tensor; those of leading dimensions of length one, which any stride describes, as 0
+    where they are not multiples of 8 anyway."""
+    st = t.stride()
+    if (st[0] | st[1] | st[2]) & 7:
+        n = t.shape
+        return tuple([0 if n[i] == 1 else st[i] for i in range(3)])
+    return st
 
 
 @dataclass(slots=True)
@@ -650,7 +653,7 @@ def fp8_quantize(x: torch.Tensor, block: int = 1, out: Fp8Code | None = None, ws
     if block not in (1, 128):
         raise ValueError("block must be 1 or 128")
     rows, cols = x.shape
-    dev = x.device
+    dev = x.get_device()
     ld, kb, rb = (cols + 15) // 16 * 16, (cols + 127) // 128, (rows + block - 1) // block
     if out is None:
         out = Fp8Code(rows, cols, block, torch.empty(rows, ld, dtype=FP8, device=dev),
@@ -676,7 +679,7 @@ def gemm_fp8(a: Fp8Code, w: Fp8Code, dtype: torch.dtype = torch.bfloat16, out: t
         raise ValueError(f"a has {a.cols} columns, w {w.cols}")
     if not a.data.is_cuda:
         raise ValueError("a must be on a CUDA device (no CPU path)")
-    M, N, K, dev = a.rows, w.rows, a.cols, a.data.device
+    M, N, K, dev = a.rows, w.rows, a.cols, a.data.get_device()
     ld, kb = (K + 15) // 16 * 16, (K + 127) // 128
     pa, psa = _on(dev, a.data, "a.data", FP8, (M, ld)), _on(dev, a.scale, "a.scale", torch.float32, (kb, M))
     pw = _on(dev, w.data, "w.data", FP8, (N, ld))
@@ -712,7 +715,7 @@ class Kv8Cache:
             raise ValueError("the cache must be on a CUDA device (no CPU path)")
         if k.dim() != 4:
             raise ValueError("cache.k must be [pages, heads, page, dim]")
-        dev, shape = k.device, k.shape
+        dev, shape = k.get_device(), k.shape
         return (_on(dev, k, "cache.k", FP8, shape), _on(dev, self.v, "cache.v", FP8, shape),
                 _on(dev, self.k_scale, "cache.k_scale", torch.float32, shape[:2]),
                 _on(dev, self.v_scale, "cache.v_scale", torch.float32, shape[:2]), *shape)
@@ -727,9 +730,9 @@ def alloc_kv8(pages: int, heads: int, dim: int = 128, page: int = 64, device=Non
                     torch.ones(pages, heads, dtype=torch.float32, device=dev))
 
 
-def _table(dev: torch.device, table: torch.Tensor, name: str) -> tuple:
-    if table.device != dev or table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
-        raise ValueError(f"{name} must be int32 [B, pages] on {dev} with contiguous rows")
+def _table(dev: int, table: torch.Tensor, name: str) -> tuple:
+    if table.get_device() != dev or table.dtype is not torch.int32 or table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
+        raise ValueError(f"{name} must be int32 [B, pages] on cuda:{dev} with contiguous rows")
     return table.data_ptr(), (table.stride(0) if table.shape[0] > 1 else table.shape[1]), table.shape[1]
 
 
@@ -738,10 +741,10 @@ def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, table: torch.T
     """Write the first n_new[b] (default: all S) tokens of k, v [B, heads, S, dim] (bf16/fp32, any strides
     of 16 bytes with dim contiguous) as slots lens[b] .. of sequence b (hq_kv8_append).  lens stays."""
     head = cache._head()
-    dev = cache.k.device
+    dev = cache.k.get_device()
     B, H, S, D = k.shape
-    if H != head[5] or D != head[7] or v.shape != k.shape or v.dtype != k.dtype or k.device != dev or v.device != dev:
-        raise ValueError(f"k and v must be [B, {head[5]}, S, {head[7]}] of one dtype on {dev}")
+    if H != head[5] or D != head[7] or v.shape != k.shape or v.dtype != k.dtype or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError(f"k and v must be [B, {head[5]}, S, {head[7]}] of one dtype on cuda:{dev}")
     ks, vs = _strides(k), _strides(v)
     if k.stride(3) != 1 or v.stride(3) != 1:
         raise ValueError("k and v need a contiguous last dimension")
@@ -771,10 +774,10 @@ def kv8_attend(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torc
     Optional outputs: lse fp32 [B, Hq, Sq]; weights fp32 [B, heads, L], the probability every slot
     received from its head's rows, added to weights_in (which may be weights itself)."""
     head = cache._head()
-    dev = cache.k.device
+    dev = cache.k.get_device()
     B, Hq, Sq, D = q.shape
-    if q.device != dev or q.dtype != torch.bfloat16 or D != head[7]:
-        raise ValueError(f"q must be bfloat16 [B, Hq, Sq, {head[7]}] on {dev}")
+    if q.get_device() != dev or q.dtype != torch.bfloat16 or D != head[7]:
+        raise ValueError(f"q must be bfloat16 [B, Hq, Sq, {head[7]}] on cuda:{dev}")
     if out is None:
         out = torch.empty(B, Hq, Sq, D, dtype=torch.bfloat16, device=dev)
     else:
@@ -821,7 +824,7 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
     (hq_kv8_evict).  Returns (out_lens [B] = min(lens, budget), out_weights [B, heads, budget], the
     kept slots' weights; entries behind out_lens are left as they were, zeros in a new tensor)."""
     head = cache._head()
-    dev = cache.k.device
+    dev = cache.k.get_device()
     B, H = lens.shape[0], head[5]
     L = weights.shape[-1]
     w = _on(dev, weights, "weights", torch.float32, (B, H, L), contiguous=False)

@@ -249,6 +249,19 @@ struct PairSmem {
     uint32_t status;
 };
 
+// Tiles in bands of PBAND rows of tiles, down each band's columns: the pairs at work share about as many
+// rows of A as of W, instead of one row of A and all of W
+constexpr int PBAND = 8;
+struct PairTile {
+    int m, n;
+};
+__device__ __forceinline__ PairTile pair_tile(int64_t tile, int MT, int NT)
+{
+    const int band = (int)(tile / ((int64_t)PBAND * NT)), rows = min(PBAND, MT - band * PBAND);
+    const int at = (int)(tile - (int64_t)band * PBAND * NT);
+    return PairTile{band * PBAND + at % rows, at / rows};
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
     gemm_fp8_pair_kernel(const F8Args a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tB)
 {
@@ -258,7 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
     const uint32_t rank = cluster_rank();
     const int KB = (int)((a.K + GK - 1) / GK);
     const int NT = (int)((a.N + PN - 1) / PN);
-    const int64_t tiles = ((a.M + 2 * GM - 1) / (2 * GM)) * NT;
+    const int MT = (int)((a.M + 2 * GM - 1) / (2 * GM));
+    const int64_t tiles = (int64_t)MT * NT;
     const int64_t tile0 = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -286,7 +300,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
             int it = 0;
             bool alive = true;
             for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
-                const int m0 = (int)(tile / NT) * 2 * GM + (int)rank * GM, n0 = (int)(tile % NT) * PN + (int)rank * GM;
+                const PairTile at = pair_tile(tile, MT, NT);
+                const int m0 = at.m * 2 * GM + (int)rank * GM, n0 = at.n * PN + (int)rank * GM;
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % PSTAGES;
                     if (it >= PSTAGES && !mbar_wait_sleep(&sm.empty[s], (uint32_t)((it / PSTAGES - 1) & 1))) {
@@ -338,7 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
         int it = 0;
         bool alive = true;
         for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
-            const int64_t m = (tile / NT) * 2 * GM + rank * GM + row, n0 = (tile % NT) * PN + 128 * h;
+            const PairTile at = pair_tile(tile, MT, NT);
+            const int64_t m = (int64_t)at.m * 2 * GM + rank * GM + row, n0 = (int64_t)at.n * PN + 128 * h;
             const float* sa = a.sa + (m < a.M ? m : 0);
             const float* sw = a.sw + n0 / 128;
             const bool some = n0 < a.N;
