@@ -125,14 +125,14 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
 // ------------------------------------------------------------------------------------------------
 // Evict, first step: which slots of a (sequence, head) stay.  The last `recent` do; of the others the
 // budget - recent with the largest weights, the lower slot first among equals.  One thread block reads
-// the weights once, as order-preserving keys in shared memory (as many as fit; the rest are read
-// again), and finds the key that divides them digit by digit: histograms of 11, 11 and 10 bits, each
+// the weights once and finds the one that divides them digit by digit over order-preserving keys: histograms of 11, 11 and 10 bits, each
 // with a scan from the largest digit down.  Then every thread takes a run of consecutive slots, counts,
 // and writes its kept ones behind those of the threads before it, so the kept slots come out in order.
 // ------------------------------------------------------------------------------------------------
 constexpr int kEThreads = 1024;
 constexpr int kEBins = 2048;
-constexpr int64_t kEKeys = 40 * 1024;  // keys held in shared memory at most (160 KB)
+constexpr int64_t kEHeld = 40 * 1024;  // weights held in shared memory at most (160 KB)
+constexpr int64_t kEPages = 4096;      // pages whose first rows are held there, if a sequence has no more
 
 struct EvictArgs {
     hq_kv8_t c;
@@ -149,7 +149,7 @@ struct EvictArgs {
     int64_t ob, oh;
     int32_t* idx;  // [B * heads, budget] cache rows of the kept slots, -1 on a page outside the pool
     uint32_t to_pages, units;
-    int page_shift, keys;
+    int page_shift, held, pages;  // weights and pages held in shared memory
     WsHeader* ws;
 };
 
@@ -194,9 +194,14 @@ __device__ __forceinline__ uint64_t block_before(uint64_t x, uint64_t* sums)
     return s - x + (warp ? sums[warp - 1] : 0ull);
 }
 
+// E > 0: up to E * 1024 weights, every thread's run of E consecutive ones in its registers; E = 0: any
+// number, from shared or global memory in every pass (the keys are made anew each time: five times the
+// instructions).
+template <int E>
 __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a)
 {
-    extern __shared__ uint32_t keys[];
+    extern __shared__ float held_w[];
+    int32_t* held_row = reinterpret_cast<int32_t*>(held_w + a.held);
     __shared__ uint32_t hist[kEBins];
     __shared__ uint32_t s_digit, s_need;
     __shared__ uint64_t sums[kEThreads / 32];
@@ -209,12 +214,19 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
     float* out_w = a.out_w ? a.out_w + b * a.ob + h * a.oh : nullptr;
     int32_t* idx = a.idx + (int64_t)blockIdx.x * a.budget;
     const int32_t* table = a.table + b * a.table_stride;
+    // first cache row of a page of the sequence, -1 outside the pool
+    auto first_row = [&](int pg) {
+        const int32_t id = __ldg(table + pg);
+        return id >= 0 && id < a.c.pages ? (int)(((uint32_t)id * a.c.heads + h) << a.page_shift) : -1;
+    };
+    for (int pg = threadIdx.x; pg < a.pages && pg << a.page_shift < n; pg += kEThreads) held_row[pg] = first_row(pg);
     auto row_of = [&](int slot) {
-        const int32_t id = __ldg(table + (slot >> a.page_shift));
-        return id >= 0 && id < a.c.pages ? (int)(((uint32_t)id * a.c.heads + h) << a.page_shift) + (slot & (a.c.page - 1)) : -1;
+        const int row = a.pages ? held_row[slot >> a.page_shift] : first_row(slot >> a.page_shift);
+        return row < 0 ? -1 : row + (slot & (a.c.page - 1));
     };
     after_me();
     if (n <= a.budget) {
+        __syncthreads();
         for (int i = threadIdx.x; i < n; i += kEThreads) {
             idx[i] = row_of(i);
             if (out_w) out_w[i] = w[i];
@@ -222,11 +234,34 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
         return;
     }
     const int recent = (int)min(a.recent, (int64_t)keep);
-    const int old = n - recent, held = min(old, a.keys);
-    auto key_at = [&](int i) { return i < held ? keys[i] : weight_key(w[i]); };
+    const int old = n - recent, held = min(old, a.held);
+    const int run = E ? E : (old + kEThreads - 1) / kEThreads;
+    const int i0 = min(old, (int)threadIdx.x * run), i1 = min(old, i0 + run);
+    float mine_w[E ? E : 1];
+    uint32_t mine_k[E ? E : 1];
+#pragma unroll
+    for (int y = 0; y < E; ++y) mine_w[y] = i0 + y < i1 ? w[i0 + y] : 0.0f;
     for (int i = threadIdx.x; i < kEBins; i += kEThreads) hist[i] = 0u;
+    if (E == 0) {
 #pragma unroll 4
-    for (int i = threadIdx.x; i < held; i += kEThreads) keys[i] = weight_key(w[i]);
+        for (int i = threadIdx.x; i < held; i += kEThreads) held_w[i] = w[i];
+    }
+#pragma unroll
+    for (int y = 0; y < E; ++y) mine_k[y] = weight_key(mine_w[y]);
+    auto weight_at = [&](int i) { return i < held ? held_w[i] : w[i]; };
+    // f(slot, key) over this thread's run, or (in any order) over a share of all slots
+    auto over_run = [&](auto f) {
+        if (E) {
+#pragma unroll
+            for (int y = 0; y < E; ++y)
+                if (i0 + y < i1) f(i0 + y, mine_k[y], mine_w[y]);
+        } else {
+            for (int i = i0; i < i1; ++i) {
+                const float x = weight_at(i);
+                f(i, weight_key(x), x);
+            }
+        }
+    };
     uint32_t need = (uint32_t)(keep - recent);  // still to find at or below the digits fixed so far
     uint32_t key = 0xFFFFFFFFu;                 // need 0: nothing lies above, none is taken at it
     __syncthreads();
@@ -237,14 +272,20 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const uint32_t digits = pass == 2 ? 1023u : 2047u;
-            for (int i = threadIdx.x; i < old; i += kEThreads) {
-                const uint32_t k = key_at(i);
-                if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & digits], 1u);
+            if (E) {
+#pragma unroll
+                for (int y = 0; y < E; ++y)
+                    if (i0 + y < i1 && (mine_k[y] & mask) == key) atomicAdd(&hist[(mine_k[y] >> shift) & digits], 1u);
+            } else {
+                for (int i = threadIdx.x; i < old; i += kEThreads) {
+                    const uint32_t k = weight_key(weight_at(i));
+                    if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & digits], 1u);
+                }
             }
             __syncthreads();
             // thread t owns digits 2047 - 2 t and 2046 - 2 t: the scan runs from the largest down
             const uint32_t d = kEBins - 1 - 2 * threadIdx.x, h0 = hist[d], h1 = hist[d - 1];
-            const uint32_t above = (uint32_t)block_before(h0 + h1, sums);
+            const uint32_t above = (uint32_t)block_before((uint64_t)(h0 + h1), sums);
             if (above < need && need <= above + h0 + h1) {
                 const bool first = need <= above + h0;
                 s_digit = first ? d : d - 1;
@@ -259,26 +300,23 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
         }
     }
     // counts of this thread's run: slots above the dividing key (high word), at it (low word)
-    const int run = (old + kEThreads - 1) / kEThreads;
-    const int i0 = min(old, (int)threadIdx.x * run), i1 = min(old, i0 + run);
-    uint64_t mine = 0;
-    for (int i = i0; i < i1; ++i) {
-        const uint32_t k = key_at(i);
-        mine += k > key ? (1ull << 32) : (k == key ? 1ull : 0ull);
-    }
-    const uint64_t before = block_before(mine, sums);
+    uint32_t over = 0, same = 0;
+    over_run([&](int, uint32_t k, float) {
+        over += k > key;
+        same += k == key;
+    });
+    const uint64_t before = block_before(((uint64_t)over << 32) | same, sums);
     uint32_t above = (uint32_t)(before >> 32), at = (uint32_t)before;
-    if (mine)
-        for (int i = i0; i < i1; ++i) {
-            const uint32_t k = key_at(i);
+    if (over | same)
+        over_run([&](int i, uint32_t k, float x) {
             if (k > key || (k == key && at < need)) {
                 const uint32_t pos = above + min(at, need);
                 idx[pos] = row_of(i);
-                if (out_w) out_w[pos] = w[i];
+                if (out_w) out_w[pos] = x;
             }
             above += k > key;
             at += k == key;
-        }
+        });
     for (int i = threadIdx.x; i < recent; i += kEThreads) {
         idx[keep - recent + i] = row_of(old + i);
         if (out_w) out_w[keep - recent + i] = w[old + i];
@@ -496,13 +534,23 @@ extern "C" hq_status_t hq_kv8_evict(const hq_kv8_evict_t* p, void* ws, size_t ws
     a.to_pages = (uint32_t)to_pages;
     a.units = (uint32_t)(p->B * p->cache.heads * to_pages);
     a.page_shift = page_shift_of(p->cache.page);
-    a.keys = (int)(p->L < kEKeys ? p->L : kEKeys);
+    const int64_t most = p->L < p->max_pages * page ? p->L : p->max_pages * page;
+    const int runs = most <= kEThreads ? 1 : (most <= 4 * kEThreads ? 4 : (most <= 8 * kEThreads ? 8 : 0));
+    a.held = runs ? 0 : (int)(most < kEHeld ? most : kEHeld);
+    a.pages = p->max_pages <= kEPages ? (int)p->max_pages : 0;
     a.ws = static_cast<WsHeader*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // set on every call: the attribute belongs to the current device's context
-    if (cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(4 * kEKeys)) != cudaSuccess)
-        return HQ_ERR_CUDA;
-    kv8_select_kernel<<<(unsigned)(p->B * p->cache.heads), kEThreads, 4 * (size_t)a.keys, st>>>(a);
+    const size_t smem = 4 * (size_t)(a.held + a.pages);
+    const unsigned blocks = (unsigned)(p->B * p->cache.heads);
+    if (runs == 1) kv8_select_kernel<1><<<blocks, kEThreads, smem, st>>>(a);
+    else if (runs == 4) kv8_select_kernel<4><<<blocks, kEThreads, smem, st>>>(a);
+    else if (runs == 8) kv8_select_kernel<8><<<blocks, kEThreads, smem, st>>>(a);
+    else {
+        // set on every call: the attribute belongs to the current device's context
+        if (cudaFuncSetAttribute(kv8_select_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(4 * (kEHeld + kEPages))) != cudaSuccess)
+            return HQ_ERR_CUDA;
+        kv8_select_kernel<0><<<blocks, kEThreads, smem, st>>>(a);
+    }
     if (cudaGetLastError() != cudaSuccess) return HQ_ERR_CUDA;
     const int grid = slots_grid(a.units);
     const cudaError_t e = p->cache.dim == 64 ? launch_move<64>(a, grid, st) : launch_move<128>(a, grid, st);

@@ -363,6 +363,12 @@ def test_evict_budgets(hq, n, budget, recent):
     check_evict(hq, 1, 2, 64, 16, [n], budget, recent, seed=n + budget)
 
 
+@pytest.mark.parametrize("n,budget", [(1024, 500), (4096, 100), (4097, 2000), (8192, 8000), (8300, 4000), (45000, 300)])
+def test_evict_long_sequences(hq, n, budget):
+    """Weights in registers (runs of 1, 4, 8), in shared memory, and more than it holds."""
+    check_evict(hq, 1, 1, 64, 128, [n], budget, 7, seed=n)
+
+
 def test_evict_ties_zeros_signs_and_nan(hq):
     def edit(w):
         w[:] = 0.0
