@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
 constexpr int kMThreads = 256;
 
 template <int D, int PASSES>
-__global__ void __launch_bounds__(kMThreads) kv8_move_kernel(const EvictArgs a)
+__global__ void __launch_bounds__(kMThreads, PASSES > 2 ? 4 : 8) kv8_move_kernel(const EvictArgs a)
 {
     constexpr int LPR = D / 16, RPP = kMThreads / LPR;
     __shared__ float s_ks[128], s_vs[128];
