@@ -394,7 +394,8 @@ hq_status_t hq_fp8_quantize(const void* x, hq_dtype_t dtype, int64_t rows, int64
  * between K and the pitch are not read), sa [ceil(K / 128), M], sw [ceil(K / 128), ceil(N / 128)] as
  * written by hq_fp8_quantize with block 1 and 128 (any finite scales are accepted), Y [M, N] bf16 or
  * fp32.  Every size from 1 up (K <= 2^20).  Block sums and the sum over blocks are binary32, in the
- * order of t.  ws may be NULL; a bounded wait that ran out reports HQ_ERR_TIMEOUT there.
+ * order of t; up to 64 rows, in up to eight parts of consecutive t whose sums are added in their order.
+ * ws may be NULL; a bounded wait that ran out reports HQ_ERR_TIMEOUT there.
  */
 hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W, int64_t ldw,
                         const float* sw, int64_t N, int64_t K, void* Y, hq_dtype_t ydtype, void* ws, size_t ws_bytes,
@@ -445,7 +446,8 @@ hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t ws_bytes, v
  * Attention over the cache: q, out [B, Hq, Sq, dim] bf16 (element strides of b, head, token; multiples
  * of 8, 16-byte aligned bases), query head i reads key head i / (Hq / heads).
  *   lens      [B] slots of each sequence (the queries' own tokens among them)
- *   q_lens    [B] queries of each sequence, NULL: Sq; rows behind them are left as they were
+ *   q_lens    [B] queries of each sequence, NULL: Sq; rows behind them are left as they were.  out may
+ *             not overlap q
  *   causal    0: a query sees all lens[b] slots; 1: query i of m sees slots 0 .. lens[b] - m + i
  *   lse       [B, Hq, Sq] fp32 (strides of b and head) natural logarithm of the sum of exp(scale q.k),
  *             or NULL.  A row that sees nothing gives zeros and -infinity.
@@ -483,8 +485,8 @@ hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t ws_bytes, v
  * Eviction by accumulated attention weight.  Of each sequence and head, the last min(recent, budget)
  * slots stay, and of the others those with the largest weights (the lower slot among equals, NaN below
  * everything) until budget slots are kept; sequences of budget slots or fewer keep all.  Each head
- * keeps its own slots.  They are moved, in order, to slots 0 .. of the pages to_table[b] (which no
- * sequence of the call reads), a new page's scale being the largest of its tokens' old ones and
+ * keeps its own slots.  They are moved, in order, to slots 0 .. of the pages to_table[b] (pages that no
+ * sequence of the call reads, each of them once), a new page's scale being the largest of its tokens' old ones and
  * codes following as in hq_kv8_append; out_lens[b] = min(lens[b], budget) (may be lens itself).
  * weights [B, heads, L] and out_weights [B, heads, >= budget] (strides of b and head; NULL: not
  * wanted; another buffer than weights) hold the slots' weights before and after.

@@ -770,7 +770,8 @@ def kv8_attend(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torc
                weights_in: torch.Tensor | None = None, ws: Workspace | None = None) -> torch.Tensor:
     """Attention of q [B, Hq, Sq, dim] bf16 (any strides of 16 bytes with dim contiguous) over the cached
     slots 0 .. lens[b] - 1 of each sequence (hq_kv8_attend); the queries are the last q_lens[b]
-    (default Sq) of them, rows behind are left as they were.  scale: 1/sqrt(dim) by default.
+    (default Sq) of them, rows behind are left as they were (in a new out: not set).  out may not be q.
+    scale: 1/sqrt(dim) by default.
     Optional outputs: lse fp32 [B, Hq, Sq]; weights fp32 [B, heads, L], the probability every slot
     received from its head's rows, added to weights_in (which may be weights itself)."""
     head = cache._head()

@@ -711,10 +711,10 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
     F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, static_cast<WsHeader*>(ws)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CUtensorMap ta, tb;
-    if (M <= 64 && slabs <= kMaxSlots / 8) {
-        // as many parts of K as fill the SMs, in powers of two up to a portable cluster
-        int parts = 1;
-        while (parts < 8 && slabs * parts * 2 <= sms && kbs >= parts * 2) parts *= 2;
+    // few rows: as many parts of K as fill the SMs, in powers of two up to a portable cluster
+    int parts = 1;
+    while (parts < 8 && slabs * parts * 2 <= sms && kbs >= parts * 2) parts *= 2;
+    if (M <= 64 && slabs * parts <= kMaxSlots) {
         const int nt = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
         if (!tensor_map_bytes(&ta, A, M, K, lda, nt) || !tensor_map_bytes(&tb, W, N, K, ldw, GM)) return HQ_ERR_CUDA;
         const cudaError_t e = nt == 16   ? launch_gemm_fp8_few<16>(a, ta, tb, parts, st)

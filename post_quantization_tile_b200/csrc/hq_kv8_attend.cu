@@ -600,7 +600,7 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
                          reinterpret_cast<uintptr_t>(p->weights) | reinterpret_cast<uintptr_t>(p->weights_in);
     if ((al & 3u) || (reinterpret_cast<uintptr_t>(ws) & 255u)) return HQ_ERR_ARG;
     if (p->weights && p->L < 1) return HQ_ERR_ARG;
-    if (p->weights_in && !p->weights) return HQ_ERR_ARG;
+    if ((p->weights_in && !p->weights) || p->out == p->q) return HQ_ERR_ARG;
     if (p->weights && p->B > 65535) return HQ_ERR_UNSUPPORTED;
     const bool many = many_rows(p->Sq * G);
     const AttendLayout l = attend_layout(p->B, p->Hq, p->Sq, p->cache.dim, p->weights != nullptr, many);

@@ -102,14 +102,14 @@ def test_append_refuses(L, bad, code):
 
 def attend(L, ws=PTR, wn=1 << 40, **d):
     h = head(d)
-    a = {**dict(q=PTR, out=PTR, B=2, Hq=4, Sq=3, st=[768, 192, 64] * 2, table=PTR, ts=4, P=4, lens=PTR, ql=0, scale=0.125, causal=1,
+    a = {**dict(q=PTR, out=2 * PTR, B=2, Hq=4, Sq=3, st=[768, 192, 64] * 2, table=PTR, ts=4, P=4, lens=PTR, ql=0, scale=0.125, causal=1,
                 lse=0, win=0, w=0, most=64), **d}
     return L.hq_kv8_attend(hq._KV8_ATTEND.pack(*h, a["q"], a["out"], a["B"], a["Hq"], a["Sq"], *a["st"], a["table"], a["ts"], a["P"],
                                                a["lens"], a["ql"], a["scale"], a["causal"], a["lse"], 12, 3, a["win"], a["w"], 128, 64,
                                                128, 64, a["most"]), ws, wn, None)
 
 
-@pytest.mark.parametrize("bad,code", HEAD_BAD + [(dict(q=0), ARG), (dict(out=0), ARG), (dict(Sq=0), ARG), (dict(Hq=5), ARG),
+@pytest.mark.parametrize("bad,code", HEAD_BAD + [(dict(q=0), ARG), (dict(out=0), ARG), (dict(out=PTR), ARG), (dict(Sq=0), ARG), (dict(Hq=5), ARG),
                                                  (dict(Hq=1), ARG), (dict(st=[768, 192, 60] * 2), ARG), (dict(q=PTR + 8), ARG),
                                                  (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
                                                  (dict(win=PTR), ARG), (dict(w=PTR, most=0), ARG), (dict(B=5000), UNSUPPORTED),

@@ -62,7 +62,7 @@ def check_attend(hq, B, H, G, Sq, D, page, lens, q_lens=None, causal=True, scale
         assert np.all(err <= do[b, :, :m] + 1e-30), (b, float((err / (do[b, :, :m] + 1e-30)).max()))
         fin = np.isfinite(rl[b, :, :m])
         assert np.array_equal(gl[b, :, :m] == -np.inf, ~fin)
-        assert np.all(np.abs(gl[b, :, :m] - rl[b, :, :m])[fin] <= dl[b, :, :m][fin] + 2.0 ** -22)
+        assert np.all(np.abs(gl[b, :, :m][fin] - rl[b, :, :m][fin]) <= dl[b, :, :m][fin] + 2.0 ** -22)
         if weights:
             gw, wi = K.values(w)[b], K.values(win)[b]
             assert np.all(gw[:, n:] == 7.0)
@@ -231,6 +231,56 @@ def test_attend_is_deterministic_and_replays_from_graphs(hq):
     lens.fill_(40)  # a replay reads the lengths of its moment
     graphs[0].replay()
     assert torch.equal(outs[0], hq.kv8_attend(q, cache, t, lens))
+
+
+def test_attend_many_rows_is_deterministic_and_replays_from_a_graph(hq):
+    g = gen(13)
+    cache, parts, table = setup_cache(hq, g, 2, 9, 2, 64, 128)
+    t, lens = i32(table), i32([560, 131])
+    q = torch.randn(2, 8, 90, 128, generator=g).to(torch.bfloat16).cuda()
+    w = [torch.zeros(2, 2, 576, device="cuda") for _ in range(2)]
+    direct = hq.kv8_attend(q, cache, t, lens, weights=w[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = hq.kv8_attend(q, cache, t, lens, weights=w[1])
+    for _ in range(3):
+        graph.replay()
+    assert torch.equal(out, direct) and torch.equal(w[1], w[0])
+    lens.fill_(100)
+    graph.replay()
+    assert torch.equal(out, hq.kv8_attend(q, cache, t, lens))
+
+
+@pytest.mark.parametrize("Sq", [1, 40])
+def test_attend_shared_pages_and_short_weights(hq, Sq):
+    """Two sequences over the same first pages; weights for fewer slots than the sequences have."""
+    g = gen(14)
+    cache, (k, v, ks, vs), table = setup_cache(hq, g, 2, 6, 2, 16, 64)
+    table[1, :4] = table[0, :4]
+    q = torch.randn(2, 4, Sq, 64, generator=g).to(torch.bfloat16).cuda()
+    w = torch.full((2, 2, 50), 7.0, device="cuda")
+    ws = hq.Workspace(hq.lib().hq_kv8_attend_workspace_bytes(2, 2, 4, Sq, 64, 1))
+    out = hq.kv8_attend(q, cache, i32(table), i32([90, 77]), weights=w, ws=ws)
+    ref, _, rw, do, _, dw = K.attend(K.values(q), k, v, ks, vs, table, [90, 77], [Sq, Sq], 0.125, True)
+    assert np.all(np.abs(K.values(out) - ref) <= do)
+    assert np.all(np.abs(K.values(w) - rw[:, :, :50]) <= dw[:, :, :50] + 2.0 ** -23 * rw[:, :, :50])
+    assert hq.status(ws)[0] == 7
+
+
+def test_attend_on_another_stream_with_a_workspace(hq):
+    g = gen(15)
+    cache, parts, table = setup_cache(hq, g, 2, 20, 2, 64, 128)
+    t, lens = i32(table), i32([1200, 40])
+    q = torch.randn(2, 4, 2, 128, generator=g).to(torch.bfloat16).cuda()
+    ref = hq.kv8_attend(q, cache, t, lens)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    ws = hq.Workspace(hq.lib().hq_kv8_attend_workspace_bytes(2, 2, 4, 2, 128, 0))
+    with torch.cuda.stream(stream):
+        for _ in range(5):
+            out = hq.kv8_attend(q, cache, t, lens, ws=ws)
+        assert hq.status(ws) == (0, 0)
+    assert torch.equal(out, ref)
 
 
 def test_calls_on_two_streams_do_not_share_scratch(hq):
@@ -410,6 +460,31 @@ def test_evict_lengths_in_place(hq):
     w = torch.rand(3, 4, 128, generator=g).cuda()
     n, _ = hq.kv8_evict(cache, i32(both[:, :8]), lens, w, 50, 10, i32(both[:, 8:]), out_lens=lens)
     assert n.data_ptr() == lens.data_ptr() and lens.cpu().tolist() == [50, 5, 50]
+
+
+def test_append_and_evict_replay_from_graphs(hq):
+    g = gen(35)
+    (a, _, both), (b, _, _) = (setup_cache(hq, gen(36), 2, 12, 2, 16, 64) for _ in range(2))
+    table, to = i32(both[:, :8]), i32(both[:, 8:])
+    x = torch.randn(2, 2, 3, 64, generator=g).to(torch.bfloat16).cuda()
+    w = torch.rand(2, 2, 128, generator=g).cuda()
+    lens = i32([70, 20])
+
+    def step(cache):
+        hq.kv8_append(cache, x, 2 * x, table, lens)
+        return hq.kv8_evict(cache, table, lens, w, 30, 5, to)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        n, ow = step(a)
+    for l in ([70, 20], [101, 64], [3, 0]):
+        lens.copy_(i32(l))
+        x *= 1.5
+        graph.replay()
+        rn, rw = step(b)
+        assert torch.equal(n, rn) and torch.equal(ow[:, :, :3], rw[:, :, :3])
+        for t, r in ((a.k, b.k), (a.v, b.v)):
+            assert torch.equal(t.view(torch.uint8), r.view(torch.uint8))
+        assert torch.equal(a.k_scale, b.k_scale) and torch.equal(a.v_scale, b.v_scale)
 
 
 # ------------------------------------------------------------------------------------------------
