@@ -2,13 +2,13 @@
 
 Every step of the codec runs in the CUDA kernels of ``libhq.so`` (built in-tree by
 ``post_quantization_tile_b200.build``).  This module only marshals torch device tensors, the
-current CUDA stream and the parameter structs into the C calls declared in ``include/hq.h``.
+current CUDA stream and the parameter structs into the C calls declared in ``include/hq.h`` (for the
+8-bit operators through the native module ``_hq8.so`` beside it).
 There is no CPU fallback: without the library or a CUDA device every call raises.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import struct
 from dataclasses import dataclass
@@ -580,51 +580,34 @@ def calibrate_step(x: torch.Tensor, tile: int, lattice: int | str, target_bps: f
 # ------------------------------------------------------------------------------------------------
 # Operators on 8-bit floating-point blocks
 # ------------------------------------------------------------------------------------------------
-# Scratch of these operators is allocated per call from torch's caching allocator on the tensors'
-# device and its current stream, so calls on several streams, and graphs captured one after the
-# other, never share it.  A Workspace passed as `ws` is used instead (its user keeps calls that share it
-# from overlapping) and receives the status that `status(ws)` reads.
+# Their marshalling is native (_hq8.so, built from csrc/hq_py.cpp next to libhq.so): a decoding step calls
+# them on a few tokens, where marshalling in Python takes as long as the kernels.  Scratch is
+# allocated per call from torch's caching allocator on the tensors' device and its current stream, so
+# calls on several streams, and graphs captured one after the other, never share it.  A Workspace
+# passed as `ws` is used instead (its user keeps calls that share it from overlapping) and receives
+# the status that `status(ws)` reads.
 FP8 = torch.float8_e4m3fn
+
+_ext = None
+
+
+def _native():
+    """Load the native marshalling of the 8-bit operators (raises if it has not been built)."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _hq8
+        except ImportError as e:
+            raise RuntimeError(f"_hq8.so is missing or unusable ({e}): run `python -m post_quantization_tile_b200.build`") from e
+        _hq8.set_error(HQError)
+        _ext = _hq8
+    return _ext
 
 
 def fp8_workspace(nbytes: int = 0, device=None) -> Workspace:
     """A Workspace for the 8-bit operators (at least what the quantizer, the GEMM and the append take)."""
     return Workspace(max(int(nbytes), lib().hq_fp8_workspace_bytes()), device=device)
-
-
-def _scratch(ws: Workspace | None, need: int, dev: int):
-    """(pointer, bytes, what keeps it alive) of a call's workspace; need = 0: none unless ws is given."""
-    if ws is not None:
-        if ws.buf.get_device() != dev:
-            raise ValueError("ws lies on another device")
-        return ws.buf.data_ptr(), ws.nbytes, ws
-    if not need:
-        return None, 0, None
-    buf = torch.empty(need, dtype=torch.uint8, device=dev)
-    return buf.data_ptr(), need, buf
-
-
-# the current stream of a device as a number (torch.cuda.current_stream builds an object first)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _on(dev: int, t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, contiguous: bool = True) -> int:
-    """data_ptr of a tensor on CUDA device `dev` after its checks."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{dev}, got {t.dtype} {list(t.shape)} on {t.device}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _strides(t: torch.Tensor) -> tuple:
-    """Strides of a 4-D tensor; those of leading dimensions of length one, which any stride describes, as 0
-    where they are not multiples of 8 anyway."""
-    st = t.stride()
-    if (st[0] | st[1] | st[2]) & 7:
-        n = t.shape
-        return tuple([0 if n[i] == 1 else st[i] for i in range(3)])
-    return st
 
 
 @dataclass(slots=True)
@@ -646,26 +629,12 @@ class Fp8Code:
 def fp8_quantize(x: torch.Tensor, block: int = 1, out: Fp8Code | None = None, ws: Workspace | None = None) -> Fp8Code:
     """Quantize a 2-D bf16/fp32 CUDA tensor (rows may be strided) to e4m3 with a power-of-two scale for
     every 1 x 128 (block 1, activations) or 128 x 128 (block 128, weights) block (hq_fp8_quantize)."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor (no CPU path)")
-    if x.dim() != 2 or x.stride(1) != 1 and x.shape[1] > 1:
-        raise ValueError("x must be 2-D [rows, cols] with contiguous rows")
-    if block not in (1, 128):
-        raise ValueError("block must be 1 or 128")
-    rows, cols = x.shape
-    dev = x.get_device()
-    ld, kb, rb = (cols + 15) // 16 * 16, (cols + 127) // 128, (rows + block - 1) // block
     if out is None:
-        out = Fp8Code(rows, cols, block, torch.empty(rows, ld, dtype=FP8, device=dev),
-                      torch.empty(kb, rb, dtype=torch.float32, device=dev))
-        q, s = out.data.data_ptr(), out.scale.data_ptr()
-    else:
-        if (out.rows, out.cols, out.block) != (rows, cols, block):
-            raise ValueError("out has another shape or block")
-        q, s = _on(dev, out.data, "out.data", FP8, (rows, ld)), _on(dev, out.scale, "out.scale", torch.float32, (kb, rb))
-    wp, wn, _keep = _scratch(ws, 0, dev)
-    _check(lib().hq_fp8_quantize(x.data_ptr(), _dtype_code(x), rows, cols, x.stride(0) if rows > 1 else cols, block, q, ld, s,
-                                 wp, wn, _raw_stream(dev)), "hq_fp8_quantize")
+        data, scale = (_ext or _native()).fp8_quantize(x, block, None, None, ws)
+        return Fp8Code(x.shape[0], x.shape[1], block, data, scale)
+    if (out.rows, out.cols, out.block) != (*x.shape, block):
+        raise ValueError("out has another shape or block")
+    _native().fp8_quantize(x, block, out.data, out.scale, ws)
     return out
 
 
@@ -677,27 +646,7 @@ def gemm_fp8(a: Fp8Code, w: Fp8Code, dtype: torch.dtype = torch.bfloat16, out: t
         raise ValueError("a must have block 1 and w block 128")
     if a.cols != w.cols:
         raise ValueError(f"a has {a.cols} columns, w {w.cols}")
-    if not a.data.is_cuda:
-        raise ValueError("a must be on a CUDA device (no CPU path)")
-    M, N, K, dev = a.rows, w.rows, a.cols, a.data.get_device()
-    ld, kb = (K + 15) // 16 * 16, (K + 127) // 128
-    pa, psa = _on(dev, a.data, "a.data", FP8, (M, ld)), _on(dev, a.scale, "a.scale", torch.float32, (kb, M))
-    pw = _on(dev, w.data, "w.data", FP8, (N, ld))
-    psw = _on(dev, w.scale, "w.scale", torch.float32, (kb, (N + 127) // 128))
-    if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=dev)
-    else:
-        _on(dev, out, "out", out.dtype, (M, N))
-    wp, wn, _keep = _scratch(ws, 0, dev)
-    _check(lib().hq_gemm_fp8(pa, ld, psa, M, pw, ld, psw, N, K, out.data_ptr(), _dtype_code(out), wp, wn, _raw_stream(dev)),
-           "hq_gemm_fp8")
-    return out
-
-
-_KV8_HEAD = "<4Qq3i4x"
-_KV8_APPEND = struct.Struct(_KV8_HEAD + "2Qi4x2q6qQ2q2Q")
-_KV8_ATTEND = struct.Struct(_KV8_HEAD + "2Q3q6qQ2q2QfiQ2q2Q4qq")
-_KV8_EVICT = struct.Struct(_KV8_HEAD + "qQ2qQQ2qq2qQ2q2Q2q")
+    return (_ext or _native()).gemm_fp8(a.rows, a.cols, a.data, a.scale, w.rows, w.data, w.scale, dtype, out, ws)
 
 
 class Kv8Cache:
@@ -709,17 +658,6 @@ class Kv8Cache:
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
 
-    def _head(self) -> tuple:
-        k = self.k
-        if not k.is_cuda:
-            raise ValueError("the cache must be on a CUDA device (no CPU path)")
-        if k.dim() != 4:
-            raise ValueError("cache.k must be [pages, heads, page, dim]")
-        dev, shape = k.get_device(), k.shape
-        return (_on(dev, k, "cache.k", FP8, shape), _on(dev, self.v, "cache.v", FP8, shape),
-                _on(dev, self.k_scale, "cache.k_scale", torch.float32, shape[:2]),
-                _on(dev, self.v_scale, "cache.v_scale", torch.float32, shape[:2]), *shape)
-
 
 def alloc_kv8(pages: int, heads: int, dim: int = 128, page: int = 64, device=None) -> Kv8Cache:
     """An empty cache of `pages` pages of `page` tokens (16, 32, 64 or 128) and heads of dim 64 or 128."""
@@ -730,38 +668,11 @@ def alloc_kv8(pages: int, heads: int, dim: int = 128, page: int = 64, device=Non
                     torch.ones(pages, heads, dtype=torch.float32, device=dev))
 
 
-def _table(dev: int, table: torch.Tensor, name: str) -> tuple:
-    if table.get_device() != dev or table.dtype is not torch.int32 or table.dim() != 2 or table.stride(1) != 1 and table.shape[1] > 1:
-        raise ValueError(f"{name} must be int32 [B, pages] on cuda:{dev} with contiguous rows")
-    return table.data_ptr(), (table.stride(0) if table.shape[0] > 1 else table.shape[1]), table.shape[1]
-
-
 def kv8_append(cache: Kv8Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
                n_new: torch.Tensor | None = None, ws: Workspace | None = None) -> None:
     """Write the first n_new[b] (default: all S) tokens of k, v [B, heads, S, dim] (bf16/fp32, any strides
     of 16 bytes with dim contiguous) as slots lens[b] .. of sequence b (hq_kv8_append).  lens stays."""
-    head = cache._head()
-    dev = cache.k.get_device()
-    B, H, S, D = k.shape
-    if H != head[5] or D != head[7] or v.shape != k.shape or v.dtype != k.dtype or k.get_device() != dev or v.get_device() != dev:
-        raise ValueError(f"k and v must be [B, {head[5]}, S, {head[7]}] of one dtype on cuda:{dev}")
-    ks, vs = _strides(k), _strides(v)
-    if k.stride(3) != 1 or v.stride(3) != 1:
-        raise ValueError("k and v need a contiguous last dimension")
-    tp, tstride, P = _table(dev, table, "table")
-    if table.shape[0] != B:
-        raise ValueError("table needs one row for each sequence")
-    wp, wn, _keep = _scratch(ws, 0, dev)
-    arg = _KV8_APPEND.pack(head[0], head[1], head[2], head[3], head[4], head[5], head[6], head[7], k.data_ptr(), v.data_ptr(),
-                           _dtype_code(k), B, S, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], tp, tstride, P,
-                           _on(dev, lens, "lens", torch.int32, (B,)),
-                           0 if n_new is None else _on(dev, n_new, "n_new", torch.int32, (B,)))
-    _check(lib().hq_kv8_append(arg, wp, wn, _raw_stream(dev)), "hq_kv8_append")
-
-
-@functools.lru_cache(maxsize=256)
-def _attend_bytes(B: int, heads: int, Hq: int, Sq: int, D: int, weights: int) -> int:
-    return lib().hq_kv8_attend_workspace_bytes(B, heads, Hq, Sq, D, weights)
+    (_ext or _native()).kv8_append(cache.k, cache.v, cache.k_scale, cache.v_scale, k, v, table, lens, n_new, ws)
 
 
 def kv8_attend(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor,
@@ -774,47 +685,8 @@ def kv8_attend(q: torch.Tensor, cache: Kv8Cache, table: torch.Tensor, lens: torc
     scale: 1/sqrt(dim) by default.
     Optional outputs: lse fp32 [B, Hq, Sq]; weights fp32 [B, heads, L], the probability every slot
     received from its head's rows, added to weights_in (which may be weights itself)."""
-    head = cache._head()
-    dev = cache.k.get_device()
-    B, Hq, Sq, D = q.shape
-    if q.get_device() != dev or q.dtype != torch.bfloat16 or D != head[7]:
-        raise ValueError(f"q must be bfloat16 [B, Hq, Sq, {head[7]}] on cuda:{dev}")
-    if out is None:
-        out = torch.empty(B, Hq, Sq, D, dtype=torch.bfloat16, device=dev)
-    else:
-        _on(dev, out, "out", torch.bfloat16, q.shape, contiguous=False)
-    qs, os_ = _strides(q), _strides(out)
-    if q.stride(3) != 1 or out.stride(3) != 1:
-        raise ValueError("q and out need a contiguous last dimension")
-    tp, tstride, P = _table(dev, table, "table")
-    if table.shape[0] != B:
-        raise ValueError("table needs one row for each sequence")
-    lp = lb = lh = wp_ = ip = wb = wh = ib = ih = L = 0
-    if lse is not None:
-        lp = _on(dev, lse, "lse", torch.float32, (B, Hq, Sq), contiguous=False)
-        lb, lh, one = lse.stride()
-        if one != 1 and Sq > 1:
-            raise ValueError("lse needs a contiguous last dimension")
-    if weights is not None:
-        L = weights.shape[-1]
-        wp_ = _on(dev, weights, "weights", torch.float32, (B, head[5], L), contiguous=False)
-        wb, wh, one = weights.stride()
-        if weights_in is not None:
-            ip = _on(dev, weights_in, "weights_in", torch.float32, (B, head[5], L), contiguous=False)
-            ib, ih, two = weights_in.stride()
-            one = max(one, two)
-        if one != 1 and L > 1:
-            raise ValueError("weights need a contiguous last dimension")
-    elif weights_in is not None:
-        raise ValueError("weights_in without weights")
-    wp, wn, _keep = _scratch(ws, _attend_bytes(B, head[5], Hq, Sq, D, weights is not None), dev)
-    arg = _KV8_ATTEND.pack(head[0], head[1], head[2], head[3], head[4], head[5], head[6], head[7], q.data_ptr(), out.data_ptr(),
-                           B, Hq, Sq, qs[0], qs[1], qs[2], os_[0], os_[1], os_[2], tp, tstride, P,
-                           _on(dev, lens, "lens", torch.int32, (B,)),
-                           0 if q_lens is None else _on(dev, q_lens, "q_lens", torch.int32, (B,)),
-                           D ** -0.5 if scale is None else scale, 1 if causal else 0, lp, lb, lh, ip, wp_, ib, ih, wb, wh, L)
-    _check(lib().hq_kv8_attend(arg, wp, wn, _raw_stream(dev)), "hq_kv8_attend")
-    return out
+    return (_ext or _native()).kv8_attend(cache.k, cache.v, cache.k_scale, cache.v_scale, q, table, lens, q_lens, scale, causal, out,
+                                          lse, weights, weights_in, ws)
 
 
 def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights: torch.Tensor, budget: int, recent: int,
@@ -824,33 +696,8 @@ def kv8_evict(cache: Kv8Cache, table: torch.Tensor, lens: torch.Tensor, weights:
     [B, heads, L] fp32, `budget` in all, and move them in order to the pages to_table [B, pages]
     (hq_kv8_evict).  Returns (out_lens [B] = min(lens, budget), out_weights [B, heads, budget], the
     kept slots' weights; entries behind out_lens are left as they were, zeros in a new tensor)."""
-    head = cache._head()
-    dev = cache.k.get_device()
-    B, H = lens.shape[0], head[5]
-    L = weights.shape[-1]
-    w = _on(dev, weights, "weights", torch.float32, (B, H, L), contiguous=False)
-    if weights.stride(2) != 1 and L > 1:
-        raise ValueError("weights need a contiguous last dimension")
-    tp, tstride, P = _table(dev, table, "table")
-    op, ostride, OP = _table(dev, to_table, "to_table")
-    if table.shape[0] != B or to_table.shape[0] != B:
-        raise ValueError("table and to_table need one row for each sequence")
-    if budget < 1 or recent < 0:
-        raise ValueError("budget must be at least 1 and recent at least 0")
-    if out_lens is None:
-        out_lens = torch.empty(B, dtype=torch.int32, device=dev)
-    if out_weights is None:
-        out_weights = torch.zeros(B, H, budget, dtype=torch.float32, device=dev)
-    if out_weights.shape[-1] < budget or out_weights.stride(-1) != 1 and budget > 1:
-        raise ValueError("out_weights needs room for the budget and a contiguous last dimension")
-    ow = _on(dev, out_weights, "out_weights", torch.float32, (B, H, out_weights.shape[-1]), contiguous=False)
-    wp, wn, _keep = _scratch(ws, lib().hq_kv8_evict_workspace_bytes(B, H, budget), dev)
-    arg = _KV8_EVICT.pack(head[0], head[1], head[2], head[3], head[4], head[5], head[6], head[7], B, tp, tstride, P,
-                          _on(dev, lens, "lens", torch.int32, (B,)), w, weights.stride(0), weights.stride(1), L, budget, recent,
-                          op, ostride, OP, _on(dev, out_lens, "out_lens", torch.int32, (B,)), ow, out_weights.stride(0),
-                          out_weights.stride(1))
-    _check(lib().hq_kv8_evict(arg, wp, wn, _raw_stream(dev)), "hq_kv8_evict")
-    return out_lens, out_weights
+    return (_ext or _native()).kv8_evict(cache.k, cache.v, cache.k_scale, cache.v_scale, table, lens, weights, budget, recent,
+                                         to_table, out_lens, out_weights, ws)
 
 
 def status(ws: Workspace) -> tuple[int, int]:

@@ -1,6 +1,7 @@
 """Builds libhq.so (the CUDA codec and its C ABI) in-tree with nvcc for sm_100a, and beside it
 libhq_test.so: the same library plus the test-only entry points of include/hq_test.h, whose
-sources are compiled again with HQ_TEST_HOOKS (the product library carries none of them).
+sources are compiled again with HQ_TEST_HOOKS (the product library carries none of them), and _hq8.so,
+the native Python marshalling of the 8-bit operators (csrc/hq_py.cpp, against the installed torch).
 
 Usage:  python -m post_quantization_tile_b200.build      (or build() from Python)
 Objects go to _build/ at the repository root; the libraries to post_quantization_tile_b200/.
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libhq.so")
 TEST_LIB = os.path.join(PKG, "libhq_test.so")
+BINDING = os.path.join(PKG, "_hq8.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
@@ -58,6 +60,25 @@ def _link(lib: str, objs: list[str], verbose: bool) -> None:
         subprocess.run(cmd, check=True)
 
 
+def _binding(verbose: bool) -> None:
+    """_hq8.so: csrc/hq_py.cpp linked with libhq.so (found beside it) and the running torch."""
+    import sysconfig
+
+    import torch
+    src, hdr = os.path.join(CSRC, "hq_py.cpp"), os.path.join(ROOT, "include", "hq.h")
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(p) for p in (src, hdr, __file__)):
+        return
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in (sysconfig.get_paths()["include"], f"{t}/include", f"{t}/include/torch/csrc/api/include", f"{cuda}/include")),
+           src, "-o", BINDING, f"-L{PKG}", "-lhq", f"-L{t}/lib", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(OBJ, exist_ok=True)
     jobs_all = [(s, False) for s in SOURCES] + [(s, True) for s in TEST_SOURCES]
@@ -67,6 +88,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     test_objs = dict(zip(TEST_SOURCES, built[len(SOURCES):]))
     _link(LIB, objs, verbose)
     _link(TEST_LIB, [test_objs.get(s, o) for s, o in zip(SOURCES, objs)], verbose)
+    _binding(verbose)
     return LIB
 
 

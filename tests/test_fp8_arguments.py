@@ -1,6 +1,10 @@
 """The 8-bit operators' argument checks (no GPU needed: refused before anything is launched), their
 argument structs, and the 64-bit definitions that the GPU tests compare with."""
 
+import os
+import struct
+import subprocess
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,11 @@ import kv8_oracle as K
 import post_quantization_tile_b200 as hq
 
 ARG, UNSUPPORTED = 1, 2
+# hq_kv8_append_t, hq_kv8_attend_t and hq_kv8_evict_t as packed bytes
+_HEAD = "<4Qq3i4x"
+APPEND = struct.Struct(_HEAD + "2Qi4x2q6qQ2q2Q")
+ATTEND = struct.Struct(_HEAD + "2Q3q6qQ2q2QfiQ2q2Q4qq")
+EVICT = struct.Struct(_HEAD + "qQ2qQQ2qq2qQ2q2Q2q")
 PTR = 4096  # an aligned address that is never read
 
 
@@ -83,7 +92,7 @@ def head(d):
 def append(L, ws=None, wn=0, **d):
     h = head(d)
     a = {**dict(xk=PTR, xv=PTR, dtype=0, B=2, S=3, st=[384, 192, 64] * 2, table=PTR, ts=4, P=4, lens=PTR, new=0), **d}
-    return L.hq_kv8_append(hq._KV8_APPEND.pack(*h, a["xk"], a["xv"], a["dtype"], a["B"], a["S"], *a["st"], a["table"], a["ts"],
+    return L.hq_kv8_append(APPEND.pack(*h, a["xk"], a["xv"], a["dtype"], a["B"], a["S"], *a["st"], a["table"], a["ts"],
                                                a["P"], a["lens"], a["new"]), ws, wn, None)
 
 
@@ -104,7 +113,7 @@ def attend(L, ws=PTR, wn=1 << 40, **d):
     h = head(d)
     a = {**dict(q=PTR, out=2 * PTR, B=2, Hq=4, Sq=3, st=[768, 192, 64] * 2, table=PTR, ts=4, P=4, lens=PTR, ql=0, scale=0.125, causal=1,
                 lse=0, win=0, w=0, most=64), **d}
-    return L.hq_kv8_attend(hq._KV8_ATTEND.pack(*h, a["q"], a["out"], a["B"], a["Hq"], a["Sq"], *a["st"], a["table"], a["ts"], a["P"],
+    return L.hq_kv8_attend(ATTEND.pack(*h, a["q"], a["out"], a["B"], a["Hq"], a["Sq"], *a["st"], a["table"], a["ts"], a["P"],
                                                a["lens"], a["ql"], a["scale"], a["causal"], a["lse"], 12, 3, a["win"], a["w"], 128, 64,
                                                128, 64, a["most"]), ws, wn, None)
 
@@ -122,7 +131,7 @@ def test_attend_refuses(L, bad, code):
 def evict(L, ws=PTR, wn=1 << 40, **d):
     h = head(d)
     a = {**dict(B=2, table=PTR, ts=4, P=4, lens=PTR, w=PTR, most=64, budget=20, recent=4, to=PTR, tos=2, top=2, ol=PTR, ow=0), **d}
-    return L.hq_kv8_evict(hq._KV8_EVICT.pack(*h, a["B"], a["table"], a["ts"], a["P"], a["lens"], a["w"], 128, 64, a["most"], a["budget"],
+    return L.hq_kv8_evict(EVICT.pack(*h, a["B"], a["table"], a["ts"], a["P"], a["lens"], a["w"], 128, 64, a["most"], a["budget"],
                                              a["recent"], a["to"], a["tos"], a["top"], a["ol"], a["ow"], 40, 20), ws, wn, None)
 
 
@@ -133,6 +142,16 @@ def test_evict_refuses(L, bad, code):
     assert evict(L, **bad) == code
 
 
+def test_packed_structs_have_the_headers_sizes(tmp_path):
+    src = tmp_path / "size.c"
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "hq.h")
+    src.write_text(f'#include <stdio.h>\n#include "{header}"\nint main(void) {{ printf("%zu %zu %zu", sizeof(hq_kv8_append_t), '
+                   "sizeof(hq_kv8_attend_t), sizeof(hq_kv8_evict_t)); return 0; }\n")
+    subprocess.run(["gcc", "-o", str(tmp_path / "size"), str(src)], check=True)
+    sizes = subprocess.run([str(tmp_path / "size")], check=True, capture_output=True, text=True).stdout.split()
+    assert sizes == [str(s.size) for s in (APPEND, ATTEND, EVICT)]
+
+
 def test_workspace_sizes(L):
     assert L.hq_fp8_workspace_bytes() >= 64 + 8 * 4096
     one = L.hq_kv8_attend_workspace_bytes(2, 4, 8, 3, 128, 0)
@@ -141,7 +160,7 @@ def test_workspace_sizes(L):
     assert L.hq_kv8_evict_workspace_bytes(2, 3, 10) >= 2 * 3 * 10 * 4 and L.hq_kv8_evict_workspace_bytes(2, 3, 0) == 0
 
 
-def test_python_refuses_cpu_tensors_and_wrong_shapes():
+def test_python_refuses_cpu_tensors_and_wrong_shapes(L):
     f8 = torch.zeros(4, 2, 16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
     cache = hq.Kv8Cache(f8, f8, torch.ones(4, 2), torch.ones(4, 2))
     i = torch.zeros(1, dtype=torch.int32)
@@ -160,6 +179,11 @@ def test_python_refuses_cpu_tensors_and_wrong_shapes():
         hq.kv8_append(cache, q, q, t, i)
     with pytest.raises(ValueError):
         hq.kv8_evict(cache, t, i, torch.zeros(1, 2, 32), 4, 1, t)
+    for bad in (None, 3, "x", [1.0]):
+        with pytest.raises(ValueError):
+            hq._native().fp8_quantize(bad, 1, None, None, None)
+    with pytest.raises(TypeError):
+        hq._native().kv8_append(1, 2)
 
 
 def test_dequantize_is_code_times_scale():
