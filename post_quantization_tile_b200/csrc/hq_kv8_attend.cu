@@ -237,7 +237,7 @@ struct AttendSmem {
     float m[kWarps][ROWS], l[kWarps][ROWS];
     float2 scale[kWarps][STAGES];  // of the group's keys and values; values < 0: no such page
     uint64_t full[kWarps][STAGES];
-    uint32_t scan[kWarps];
+    uint64_t scan[kWarps];
     uint32_t status;
 };
 
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
     if (share_prefix<U, kThreadsA>(a, pre, sm.scan) && blockIdx.x == 0) atomicOr(&sm.status, kStRange);
     after_me();
     const uint32_t W = pre[a.B];
-    const uint32_t shares = share_count(W, gridDim.x);
+    const uint32_t shares = pre[a.B + 1];
     uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
     const uint32_t w1 = blockIdx.x < shares ? (uint32_t)((uint64_t)(blockIdx.x + 1) * W / shares) : 0u;
     uint32_t status = 0u;
@@ -296,7 +296,6 @@ __global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
                 }
             }
             if (lane == (i & 31)) {  // the lane that knows the group issues it
-                sm.scale[warp][st] = my_scale;
                 if (my_row >= 0) {
                     mbar_arrive_expect_tx(&sm.full[warp][st], 32 * D);
                     tma_load_2d(sm.ring[warp][st][0], &tk, 0, my_row, &sm.full[warp][st]);
@@ -304,6 +303,7 @@ __global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
                 } else {
                     mbar_arrive(&sm.full[warp][st]);
                 }
+                sm.scale[warp][st] = my_scale;  // may still be on its way when the boxes are asked for
             }
         };
         {
@@ -526,7 +526,7 @@ AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool we
     const size_t parts = many ? (size_t)2 * kMaxGridMany * kManyRows : (size_t)2 * kMaxGridFew * 16;
     AttendLayout l;
     l.prefix = align256(kSlotBytes);
-    l.part_o = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 1));
+    l.part_o = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 2));
     l.part_ml = l.part_o + parts * (size_t)D * sizeof(float);
     l.lse2 = l.part_ml + parts * sizeof(float2);
     l.bytes = l.lse2 + (weights ? align256(sizeof(float) * (size_t)(B * Hq * Sq)) : 0);
@@ -539,14 +539,14 @@ cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
     CUtensorMap tk, tv;
     const int64_t rows = a.c.pages * a.c.heads * a.c.page;
     if (!tensor_map_kv8(&tk, a.c.k, rows, D, 16) || !tensor_map_kv8(&tv, a.c.v, rows, D, 16)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + sizeof(AttendSmem<D, ROWS>) + sizeof(uint32_t) * (size_t)(a.B + 1);
+    const size_t smem = 1024 + sizeof(AttendSmem<D, ROWS>) + sizeof(uint32_t) * (size_t)(a.B + 2);
     cudaError_t e = cudaFuncSetAttribute(kv8_attend_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int grid = min(FewCfg<ROWS>::BLOCKS * num_sms(), kMaxGridFew);
     kv8_attend_kernel<D, ROWS><<<grid, kThreadsA, smem, st>>>(a, tk, tv);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rts = (a.Sq * a.G + ROWS - 1) / ROWS;
-    return launch_after(kv8_join_kernel<D, FewRows<ROWS>>, dim3((unsigned)(a.B * a.c.heads * rts)), kJoinThreads<D, ROWS>, 0, st, a, rts, grid);
+    return launch_after(kv8_join_kernel<D, FewRows<ROWS>>, dim3((unsigned)(a.B * a.c.heads * rts)), kJoinThreads<D, ROWS>, 0, st, a, rts);
 }
 
 template <int D>

@@ -29,7 +29,7 @@ struct AttendArgs {
     const float* win;
     float* w;
     int64_t wib, wih, wb, wh, L;
-    uint32_t* prefix;  // [B + 1] share units before each sequence
+    uint32_t* prefix;  // [B + 2] tiles before each sequence, of all, and the number of shares
     float* part_o;     // [2 grid][rows of a unit][D]
     float2* part_ml;   // [2 grid][rows of a unit]
     float* lse2;       // [B][heads][G Sq] binary logarithm of the sums (weights only)
@@ -98,49 +98,56 @@ __device__ __forceinline__ void write_lse(const AttendArgs& a, int b, int h, int
 // U::TILE slots.  All units' tiles are laid end to end (sequences, then heads, then row tiles) and cut
 // into equal shares, one per thread block.
 // ------------------------------------------------------------------------------------------------
-// prefix sums of the sequences' tiles into `pre` [B + 1] (shared memory; block 0 also leaves them for the
-// join); `scan` holds one value per warp.  Returns whether this thread met a length out of range.
+// Number of shares of W tiles in `units` units over `grid` thread blocks.  None is empty (the join walks a
+// unit's shares one by one).  Few tiles are cut into fewer shares than thread blocks: a share of n tiles
+// takes time with n, a unit of T tiles is joined in time with T / n, so n is about the root of T (8192
+// slots of two heads: 26.9 us with shares of 2 tiles, 16.7 with 8; 1000 slots of eight heads: 10.6, 12.8).
+__device__ __forceinline__ uint32_t share_count(uint32_t W, uint32_t units, uint32_t grid)
+{
+    const uint32_t n = max(2u, (uint32_t)sqrtf((float)W / (float)max(units, 1u)));
+    return min((W + n - 1) / n, grid);
+}
+
+// prefix sums of the sequences' tiles into `pre` [B + 1] (shared memory), the number of shares into
+// pre[B + 1]; block 0 also leaves them for the join.  `scan` holds one value per warp.  Returns whether
+// this thread met a length out of range.
 template <class U, int THREADS>
-__device__ __forceinline__ bool share_prefix(const AttendArgs& a, uint32_t* pre, uint32_t* scan)
+__device__ __forceinline__ bool share_prefix(const AttendArgs& a, uint32_t* pre, uint64_t* scan)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int run = (a.B + THREADS - 1) / THREADS, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
-    uint32_t mine = 0, last = 0;
+    uint64_t mine = 0;  // units (high word) and tiles
+    uint32_t last = 0;
     bool odd = false;
     for (int b = b0; b < b1; ++b) {
         const SeqLen s = seq_len(a, b);
         odd |= s.odd;
         last = U::of_sequence(a, s);
-        mine += last;
+        mine += last + ((uint64_t)(last ? a.c.heads * U::row_tiles(a, s.m) : 0) << 32);
     }
-    uint32_t inc = mine;
+    uint64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        const uint64_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
         if (lane >= o) inc += x;
     }
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    uint32_t at = inc - mine;
-    for (int i = 0; i < warp; ++i) at += scan[i];
+    uint64_t before = inc - mine;
+    for (int i = 0; i < warp; ++i) before += scan[i];
+    uint32_t at = (uint32_t)before;
     for (int b = b0; b < b1; ++b) {
         pre[b] = at;
         at += b1 - b0 == 1 ? last : U::of_sequence(a, seq_len(a, b));
     }
-    if (tid == THREADS - 1) pre[a.B] = at;
+    if (tid == THREADS - 1) {
+        pre[a.B] = at;
+        pre[a.B + 1] = share_count(at, (uint32_t)((before + mine) >> 32), gridDim.x);
+    }
     __syncthreads();
     if (blockIdx.x == 0)
-        for (int b = tid; b <= a.B; b += THREADS) a.prefix[b] = pre[b];
+        for (int b = tid; b <= a.B + 1; b += THREADS) a.prefix[b] = pre[b];
     return odd;
-}
-
-// Shares of W tiles over `grid` thread blocks: none is empty (the join walks a unit's shares one by one),
-// and none is so short that joining costs more than it saves.
-constexpr uint32_t kShareTiles = 2;
-__host__ __device__ __forceinline__ uint32_t share_count(uint32_t W, uint32_t grid)
-{
-    const uint32_t most = (W + kShareTiles - 1) / kShareTiles;
-    return most < grid ? most : grid;
 }
 
 // the part of a thread block's share [w0, w1) that lies in the unit of tile w0
@@ -174,7 +181,7 @@ template <int D, int ROWS>
 constexpr int kJoinThreads = D / 4 * kJoinRows<ROWS>;
 
 template <int D, class U>
-__global__ void __launch_bounds__((kJoinThreads<D, U::R>)) kv8_join_kernel(const AttendArgs a, int row_tiles_max, int grid)
+__global__ void __launch_bounds__((kJoinThreads<D, U::R>)) kv8_join_kernel(const AttendArgs a, int row_tiles_max)
 {
     constexpr int JR = kJoinRows<U::R>, TPR = D / 4;
     const int jr = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__((kJoinThreads<D, U::R>)) kv8_join_kernel(const
     if (!rows) return;
     const uint32_t W = a.prefix[a.B], w0 = a.prefix[b] + before, w1 = w0 + tiles;
     // the share that holds tile w: the smallest c with w < floor((c + 1) W / shares)
-    const uint32_t shares = share_count(W, (uint32_t)grid);
+    const uint32_t shares = a.prefix[a.B + 1];
     const int c0 = tiles ? (int)(((uint64_t)(w0 + 1) * shares - 1) / W) : 0;
     const int c1 = tiles ? (int)(((uint64_t)w1 * shares - 1) / W) : -1;
     if (tiles && c0 == c1) return;  // whole: written already

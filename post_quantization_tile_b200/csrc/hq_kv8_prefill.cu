@@ -79,7 +79,7 @@ struct PrefillSmem {
     uint64_t q_ready[2], drain;
     uint32_t tmem_base;
     uint32_t status;
-    uint32_t scan[kThreadsP / 32];
+    uint64_t scan[kThreadsP / 32];
 };
 
 // sixteen codes of a row (16-byte chunk c of 64) as binary16, times r2, into a swizzled operand run.  The
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
     after_me();
     const uint32_t tbase = sm.tmem_base;
     const uint32_t W = pre[a.B];
-    const uint32_t shares = share_count(W, gridDim.x);
+    const uint32_t shares = pre[a.B + 1];
     uint32_t w0 = blockIdx.x < shares ? (uint32_t)((uint64_t)blockIdx.x * W / shares) : 0u;
     const uint32_t w1 = blockIdx.x < shares ? (uint32_t)((uint64_t)(blockIdx.x + 1) * W / shares) : 0u;
     // After a wait that ran out a warp only walks its loops, without waiting or working.
@@ -493,13 +493,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
 template <int D>
 cudaError_t launch_many(const AttendArgs& a, int grid, cudaStream_t st)
 {
-    const size_t smem = 1024 + sizeof(PrefillSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 1);
+    const size_t smem = 1024 + sizeof(PrefillSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 2);
     cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kv8_prefill_kernel<D><<<grid, kThreadsP, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int rts = (a.Sq * a.G + 15) / 16;
-    return launch_after(kv8_join_kernel<D, ManyRows>, dim3((unsigned)(a.B * a.c.heads * rts)), kJoinThreads<D, kManyRows>, 0, st, a, rts, grid);
+    return launch_after(kv8_join_kernel<D, ManyRows>, dim3((unsigned)(a.B * a.c.heads * rts)), kJoinThreads<D, kManyRows>, 0, st, a, rts);
 }
 
 }  // namespace
