@@ -479,6 +479,7 @@ struct FewCfg {
     static constexpr int ACC = 256 / NT;  // accumulator slots in 256 TMEM columns
 };
 constexpr int kFewThreads = 192;  // producer, MMA issue, four epilogue warps
+constexpr int kFewChunk = 8;      // blocks whose scales are fetched at a time
 
 template <int NT>
 struct FewSmem {
@@ -486,7 +487,7 @@ struct FewSmem {
     alignas(1024) uint8_t w[C::STAGES][GM * GK];
     alignas(1024) uint8_t a[C::STAGES][NT * GK];
     alignas(16) float red[NT * GM];      // [source rank][column of this CTA's share][row of W]
-    alignas(16) float factor[4][2][NT];  // of a block's columns, by epilogue warp and parity
+    alignas(16) float factor[2][kFewChunk][NT];  // sa sw of the columns, for a chunk of blocks and the next
     alignas(8) uint64_t full[C::STAGES];
     uint64_t empty[C::STAGES];
     uint64_t acc_full[C::ACC];
@@ -581,33 +582,40 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     float2 acc[NT / 2];
     const int q = warp & 3, row = q * 32 + lane;
     if (warp >= 2) {
-        // one row of W per thread; the columns' factors sa sw go through shared memory, one per lane
+        // One row of W per thread.  The columns' factors sa sw go through shared memory, a chunk of blocks at
+        // a time with the next chunk's under way: a block takes less time than fetching its scales.
         const int64_t NB = (a.N + 127) / 128;
         const float* sw = a.sw + n0 / 128;
 #pragma unroll
         for (int c = 0; c < NT / 2; ++c) acc[c] = make_float2(0.0f, 0.0f);
-        constexpr int PER = (NT + 31) / 32;
+        constexpr int PER = kFewChunk * NT / 128;
         float next[PER];
-        auto fetch = [&](int kb) {
+        const int et = (int)threadIdx.x - 64;
+        auto fetch = [&](int kb0) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int m = lane + 32 * i;
-                next[i] = m < NT && m < a.M && kb < k1 ? __ldg(a.sa + (int64_t)kb * a.M + m) * __ldg(sw + (int64_t)kb * NB) : 0.0f;
+                const int m = (et + 128 * i) % NT, kb = kb0 + (et + 128 * i) / NT;
+                next[i] = m < a.M && kb < k1 ? __ldg(a.sa + (int64_t)kb * a.M + m) * __ldg(sw + (int64_t)kb * NB) : 0.0f;
             }
         };
         fetch(k0);
+        bool alive = true;  // after a timeout a warp only walks on, so that all reach the named barrier
         for (int it = 0; it < k1 - k0; ++it) {
-            const int slot = it % C::ACC;
-            float* factor = sm.factor[q][it & 1];
+            const int slot = it % C::ACC, chunk = it / kFewChunk;
+            if (it % kFewChunk == 0) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (lane + 32 * i < NT) factor[lane + 32 * i] = next[i];
-            fetch(k0 + it + 1);
+                for (int i = 0; i < PER; ++i) sm.factor[chunk & 1][0][et + 128 * i] = next[i];
+                named_sync(1, 128);
+                fetch(k0 + it + kFewChunk);
+            }
+            if (!alive) continue;
+            const float* factor = sm.factor[chunk & 1][it % kFewChunk];
             const bool got = mbar_wait_sleep(&sm.acc_full[slot], (uint32_t)((it / C::ACC) & 1));
             __syncwarp();
             if (!__all_sync(0xFFFFFFFFu, got)) {
                 if (lane == 0) atomicOr(&sm.status, kStTimeout);
-                break;
+                alive = false;
+                continue;
             }
             tc_fence_after();
             uint32_t S[NT];
@@ -627,7 +635,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     // the parts' sums: column c to the CTA that owns it
     const int share = NT / parts;
-    if (parts > 1) cluster_sync();  // every CTA of the cluster is up (long since)
+    if (parts > 1) cluster_sync();  // every CTA of the cluster is up (an arrival at the start and a wait here: slower)
     if (warp >= 2) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
