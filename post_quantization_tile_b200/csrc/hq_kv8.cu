@@ -36,28 +36,35 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
 {
     constexpr int LPR = D / 8;                // lanes of one row
     constexpr int RPP = kAThreads / LPR;      // rows of one pass
-    __shared__ uint32_t warp_max[2][kAThreads / 32];
+    // by turns, so that one barrier a unit (between the maxima and their use) suffices
+    __shared__ uint32_t warp_max[2][2][kAThreads / 32];
     __shared__ uint32_t s_status, s_nonfinite;
     const int sub = threadIdx.x % LPR, row = threadIdx.x / LPR;
     if (threadIdx.x == 0) s_status = 0u, s_nonfinite = 0u;
-    __syncthreads();
     const int page = a.c.page;
-    for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x) {
+    __syncthreads();
+    int turn = 0;
+    for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x, turn ^= 1) {
         const uint32_t bh = u / a.span, sp = u - bh * a.span;
         const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * a.c.heads);
+        // Every thread reaches the unit's one barrier, whatever the lengths and the table it read, and touches
+        // only what they allow.
         const int64_t first = a.lens[b];
         int64_t n = a.n_new ? (int64_t)a.n_new[b] : a.S;
         const bool odd = first < 0 || n < 0 || n > a.S || first + n > a.max_pages * page;
         if (odd && threadIdx.x == 0 && sp == 0) atomicOr(&s_status, kStRange);
         n = min(n, a.S);
-        if (first < 0 || n <= 0) continue;
-        const int64_t at = first / page + sp;             // page of the sequence
+        const int64_t at = first < 0 ? a.max_pages : first / page + sp;  // page of the sequence
         const int64_t lo64 = max(first, at * page), hi64 = min(first + n, (at + 1) * page);
-        if (at >= a.max_pages || lo64 >= hi64) continue;
-        const int lo = (int)(lo64 - at * page), hi = (int)(hi64 - at * page);
-        const int32_t id = a.table[b * a.table_stride + at];
+        const bool some = at < a.max_pages && lo64 < hi64;
+        const int lo = some ? (int)(lo64 - at * page) : 0, hi = some ? (int)(hi64 - at * page) : 0;
+        const int32_t id = some ? a.table[b * a.table_stride + at] : -1;
         // the new rows are on their way before the page is known
         Raw8<T> v[2][PASSES];
+        if (!__any_sync(0xFFFFFFFFu, some)) {
+            __syncthreads();
+            continue;
+        }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
             const T* x = static_cast<const T*>(a.x[kv]) + b * a.sb[kv] + h * a.sh[kv] + (at * page - first) * a.ss[kv];
@@ -68,12 +75,10 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
                 if (r >= lo && r < hi) v[kv][p].load(x + r * a.ss[kv] + sub * 8);
             }
         }
-        if (id < 0 || id >= a.c.pages) {
-            if (threadIdx.x == 0) atomicOr(&s_status, kStRange);
-            continue;
-        }
-        const int64_t ph = (int64_t)id * a.c.heads + h;
-        const float s_old[2] = {lo > 0 ? a.c.k_scale[ph] : 0.0f, lo > 0 ? a.c.v_scale[ph] : 0.0f};
+        const bool good = id >= 0 && id < a.c.pages;
+        if (some && !good && threadIdx.x == 0) atomicOr(&s_status, kStRange);
+        const int64_t ph = good ? (int64_t)id * a.c.heads + h : 0;
+        const float s_old[2] = {good && lo > 0 ? a.c.k_scale[ph] : 0.0f, good && lo > 0 ? a.c.v_scale[ph] : 0.0f};
         uint32_t top[2] = {0u, 0u};
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -90,13 +95,14 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
                 top[kv] = max(top[kv], m);
             }
             top[kv] = __reduce_max_sync(0xFFFFFFFFu, top[kv]);
-            if ((threadIdx.x & 31) == 0) warp_max[kv][threadIdx.x >> 5] = top[kv];
+            if ((threadIdx.x & 31) == 0) warp_max[turn][kv][threadIdx.x >> 5] = top[kv];
         }
         __syncthreads();  // also: every thread has read the old scales
+        if (!good) continue;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
-            for (int w = 0; w < kAThreads / 32; ++w) top[kv] = max(top[kv], warp_max[kv][w]);
+            for (int w = 0; w < kAThreads / 32; ++w) top[kv] = max(top[kv], warp_max[turn][kv][w]);
             if (top[kv] > kAmaxLimit && threadIdx.x == 0) atomicOr(&s_status, kStRange);
             const float s_new = fmaxf(s_old[kv], exp2_int(scale_exp(top[kv])));
             if (threadIdx.x == 0 && s_new != s_old[kv]) (kv ? a.c.v_scale : a.c.k_scale)[ph] = s_new;
@@ -116,7 +122,6 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
                 }
             }
         }
-        __syncthreads();  // warp_max is written again by the next unit
     }
     __syncthreads();
     if (threadIdx.x == 0) slot_write(a.ws, gridDim.x, blockIdx.x, s_status, s_nonfinite);
@@ -125,9 +130,11 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
 // ------------------------------------------------------------------------------------------------
 // Evict, first step: which slots of a (sequence, head) stay.  The last `recent` do; of the others the
 // budget - recent with the largest weights, the lower slot first among equals.  One thread block reads
-// the weights once and finds the one that divides them digit by digit over order-preserving keys: histograms of 11, 11 and 10 bits, each
-// with a scan from the largest digit down.  Then every thread takes a run of consecutive slots, counts,
-// and writes its kept ones behind those of the threads before it, so the kept slots come out in order.
+// the weights once and finds the one that divides them digit by digit over order-preserving keys:
+// histograms of 11, 11 and 10 bits, each with a scan from the largest digit down.  Then every thread
+// takes a run of consecutive slots, counts, and writes its kept ones behind those of the threads before
+// it, so the kept slots come out in order.  Up to 8192 slots stay in registers (8 x 32 heads x 8192:
+// about 20 us, bound by instructions; from shared memory 26 us).
 // ------------------------------------------------------------------------------------------------
 constexpr int kEThreads = 1024;
 constexpr int kEBins = 2048;
@@ -207,9 +214,13 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
     __shared__ uint64_t sums[kEThreads / 32];
     const int h = blockIdx.x % a.c.heads;
     const int64_t b = blockIdx.x / a.c.heads;
-    bool odd;
-    const int n = (int)kept_len(a, b, odd);
-    const int keep = (int)min((int64_t)n, a.budget);
+    __shared__ int s_n;
+    if (threadIdx.x == 0) {  // read once: the whole block takes the same way
+        bool odd;
+        s_n = (int)kept_len(a, b, odd);
+    }
+    __syncthreads();
+    const int n = s_n, keep = (int)min((int64_t)n, a.budget);
     const float* w = a.w + b * a.wb + h * a.wh;
     float* out_w = a.out_w ? a.out_w + b * a.ob + h * a.oh : nullptr;
     int32_t* idx = a.idx + (int64_t)blockIdx.x * a.budget;
@@ -335,19 +346,26 @@ __global__ void __launch_bounds__(kMThreads, PASSES > 2 ? 4 : 8) kv8_move_kernel
     constexpr int LPR = D / 16, RPP = kMThreads / LPR;
     __shared__ float s_ks[128], s_vs[128];
     __shared__ uint32_t s_top[2], s_status;
+    __shared__ int64_t s_n;
     const int page = a.c.page;
     const int sub = threadIdx.x % LPR, row = threadIdx.x / LPR;
-    if (threadIdx.x == 0) s_status = 0u, s_top[0] = 0u, s_top[1] = 0u;
-    __syncthreads();
+    const int32_t all_rows = (int32_t)((a.c.pages * a.c.heads) << a.page_shift);
+    if (threadIdx.x == 0) s_status = 0u;
     wait_before_me();  // the kept rows
     for (uint32_t u = blockIdx.x; u < a.units; u += gridDim.x) {
         const uint32_t bh = u / a.to_pages, pg = u - bh * a.to_pages;
         const int b = (int)(bh / (uint32_t)a.c.heads), h = (int)(bh - (uint32_t)b * a.c.heads);
-        bool odd;
-        const int64_t n = min(kept_len(a, b, odd), a.budget);
-        if (odd && threadIdx.x == 0) atomicOr(&s_status, kStRange);
-        // out_lens may be lens itself: every reader takes min(lens, budget), the value written here
-        if (pg == 0 && h == 0 && threadIdx.x == 0) a.out_lens[b] = (int32_t)n;
+        __syncthreads();
+        if (threadIdx.x == 0) {  // read once: the whole block takes the same way
+            bool odd;
+            s_n = min(kept_len(a, b, odd), a.budget);
+            s_top[0] = s_top[1] = 0u;
+            if (odd) s_status |= kStRange;
+            // out_lens may be lens itself: every reader takes min(lens, budget), the value written here
+            if (pg == 0 && h == 0) a.out_lens[b] = (int32_t)s_n;
+        }
+        __syncthreads();
+        const int64_t n = s_n;
         const int rows = (int)min((int64_t)page, n - (int64_t)pg * page);
         if (rows <= 0) continue;
         const int32_t id = a.to[b * a.to_stride + pg];
@@ -357,13 +375,14 @@ __global__ void __launch_bounds__(kMThreads, PASSES > 2 ? 4 : 8) kv8_move_kernel
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
             const int r = p * RPP + row, at = r < rows ? from[r] : -1;
-            if (at >= 0) {
+            if (at >= 0 && at < all_rows) {
                 q[0][p] = *reinterpret_cast<const uint4*>(a.c.k + (int64_t)at * D + sub * 16);
                 q[1][p] = *reinterpret_cast<const uint4*>(a.c.v + (int64_t)at * D + sub * 16);
             }
         }
         uint32_t ktop = 0, vtop = 0;  // positive floats order like their bit patterns
-        if ((int)threadIdx.x < rows && mine >= 0) {
+        const bool good = mine >= 0 && mine < all_rows;  // a row that the selection wrote, on a page of the pool
+        if ((int)threadIdx.x < rows && good) {
             const float ks = a.c.k_scale[mine >> a.page_shift], vs = a.c.v_scale[mine >> a.page_shift];
             s_ks[threadIdx.x] = ks;
             s_vs[threadIdx.x] = vs;
@@ -373,9 +392,8 @@ __global__ void __launch_bounds__(kMThreads, PASSES > 2 ? 4 : 8) kv8_move_kernel
         ktop = __reduce_max_sync(0xFFFFFFFFu, ktop);
         vtop = __reduce_max_sync(0xFFFFFFFFu, vtop);
         if ((threadIdx.x & 31) == 0 && (ktop | vtop)) atomicMax(&s_top[0], ktop), atomicMax(&s_top[1], vtop);
-        if (__syncthreads_or(mine < 0 || id < 0 || id >= a.c.pages)) {  // a page outside the pool: left as it was
-            if (threadIdx.x == 0) atomicOr(&s_status, kStRange), s_top[0] = 0u, s_top[1] = 0u;
-            __syncthreads();
+        if (__syncthreads_or(!good || id < 0 || id >= a.c.pages)) {  // a page outside the pool: left as it was
+            if (threadIdx.x == 0) s_status |= kStRange;
             continue;
         }
         const float kto = __uint_as_float(s_top[0]), vto = __uint_as_float(s_top[1]);
@@ -398,9 +416,6 @@ __global__ void __launch_bounds__(kMThreads, PASSES > 2 ? 4 : 8) kv8_move_kernel
             }
         }
         if (threadIdx.x == 0) a.c.k_scale[to] = kto, a.c.v_scale[to] = vto;
-        __syncthreads();
-        if (threadIdx.x == 0) s_top[0] = 0u, s_top[1] = 0u;
-        __syncthreads();
     }
     __syncthreads();
     if (threadIdx.x == 0) slot_write(a.ws, gridDim.x, blockIdx.x, s_status, 0u);
@@ -446,7 +461,7 @@ extern "C" hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t 
     if (p->dtype != HQ_BF16 && p->dtype != HQ_F32) return HQ_ERR_ARG;
     if (!kv8_shape_supported(&p->cache)) return HQ_ERR_UNSUPPORTED;
     if (p->B < 1 || p->S < 1 || p->max_pages < 1 || p->table_stride < p->max_pages) return HQ_ERR_ARG;
-    if (p->B > ((int64_t)1 << 24) || p->S > ((int64_t)1 << 31) || p->max_pages > ((int64_t)1 << 24)) return HQ_ERR_ARG;
+    if (p->B > ((int64_t)1 << 24) || p->S > ((int64_t)1 << 31) - 1 || p->max_pages > ((int64_t)1 << 24)) return HQ_ERR_ARG;
     const int64_t es = p->dtype == HQ_BF16 ? 2 : 4;
     const int64_t strides = p->k_stride[0] | p->k_stride[1] | p->k_stride[2] | p->v_stride[0] | p->v_stride[1] | p->v_stride[2];
     const uintptr_t bases = reinterpret_cast<uintptr_t>(p->k) | reinterpret_cast<uintptr_t>(p->v);

@@ -470,19 +470,17 @@ __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendA
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int h = blockIdx.y, b = blockIdx.z;
-    const SeqLen s = seq_len(a, b);
-    const int n = (int)min((int64_t)s.n, a.L);
     const int tok = (blockIdx.x * kWarps + warp) * 16;
-    if (tok >= n) {
-        wait_before_me();  // in every block, so that this grid never ends before those it follows
-        return;
-    }
+    wait_before_me();  // in every block, so that this grid never ends before those it follows
+    const int2 len = a.len[b];
+    const SeqLen s{len.x, len.y, false};
+    const int n = (int)min((int64_t)s.n, a.L);
+    if (tok >= n) return;
     const int row = locate(a, a.table + b * a.table_stride, h, tok);
     const bool ok = row >= 0;
     KeyGroup<D> k;
     k.load_global(a.c.k + (int64_t)(ok ? row : 0) * D, ok);
     const float ks = ok ? __ldg(a.c.k_scale + (row >> a.page_shift)) : 0.0f;
-    wait_before_me();  // the rows' sums
     float sum[2] = {0.0f, 0.0f};
     const float* lse2 = a.lse2 + ((int64_t)b * a.c.heads + h) * a.G * a.Sq;
     const int rows = s.m * a.G;
@@ -519,14 +517,15 @@ bool many_rows(int64_t rows) { return rows > 16; }
 constexpr int kMaxGridFew = 512, kMaxGridMany = 256;
 
 struct AttendLayout {
-    size_t prefix, part_o, part_ml, lse2, bytes;
+    size_t prefix, len, part_o, part_ml, lse2, bytes;
 };
 AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool weights, bool many)
 {
     const size_t parts = many ? (size_t)2 * kMaxGridMany * kManyRows : (size_t)2 * kMaxGridFew * 16;
     AttendLayout l;
     l.prefix = align256(kSlotBytes);
-    l.part_o = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 2));
+    l.len = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 2));
+    l.part_o = l.len + align256(sizeof(int2) * (size_t)B);
     l.part_ml = l.part_o + parts * (size_t)D * sizeof(float);
     l.lse2 = l.part_ml + parts * sizeof(float2);
     l.bytes = l.lse2 + (weights ? align256(sizeof(float) * (size_t)(B * Hq * Sq)) : 0);
@@ -539,7 +538,7 @@ cudaError_t launch_few(const AttendArgs& a, cudaStream_t st)
     CUtensorMap tk, tv;
     const int64_t rows = a.c.pages * a.c.heads * a.c.page;
     if (!tensor_map_kv8(&tk, a.c.k, rows, D, 16) || !tensor_map_kv8(&tv, a.c.v, rows, D, 16)) return cudaErrorInvalidValue;
-    const size_t smem = 1024 + sizeof(AttendSmem<D, ROWS>) + sizeof(uint32_t) * (size_t)(a.B + 2);
+    const size_t smem = 1024 + sizeof(AttendSmem<D, ROWS>) + share_bytes(a.B);
     cudaError_t e = cudaFuncSetAttribute(kv8_attend_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int grid = min(FewCfg<ROWS>::BLOCKS * num_sms(), kMaxGridFew);
@@ -641,6 +640,7 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     a.L = p->L;
     char* base = static_cast<char*>(ws);
     a.prefix = reinterpret_cast<uint32_t*>(base + l.prefix);
+    a.len = reinterpret_cast<int2*>(base + l.len);
     a.part_o = reinterpret_cast<float*>(base + l.part_o);
     a.part_ml = reinterpret_cast<float2*>(base + l.part_ml);
     a.lse2 = p->weights ? reinterpret_cast<float*>(base + l.lse2) : nullptr;

@@ -5,7 +5,7 @@
 
 namespace hq {
 
-constexpr int kMaxBatch = 4096;   // sequences of one call (their prefix sums live in shared memory)
+constexpr int kMaxBatch = 2048;   // sequences of one call (their prefix sums live in shared memory)
 constexpr float kBoost = 7.0f;    // probabilities are held times 2^7, and up to 2^8 times that
 constexpr float kSlack = 8.0f;    // before a larger maximum moves the reference they are relative to
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -30,6 +30,7 @@ struct AttendArgs {
     float* w;
     int64_t wib, wih, wb, wh, L;
     uint32_t* prefix;  // [B + 2] tiles before each sequence, of all, and the number of shares
+    int2* len;         // [B] the lengths (slots, queries) that the first block read
     float* part_o;     // [2 grid][rows of a unit][D]
     float2* part_ml;   // [2 grid][rows of a unit]
     float* lse2;       // [B][heads][G Sq] binary logarithm of the sums (weights only)
@@ -108,12 +109,19 @@ __device__ __forceinline__ uint32_t share_count(uint32_t W, uint32_t units, uint
     return min((W + n - 1) / n, grid);
 }
 
-// prefix sums of the sequences' tiles into `pre` [B + 1] (shared memory), the number of shares into
-// pre[B + 1]; block 0 also leaves them for the join.  `scan` holds one value per warp.  Returns whether
-// this thread met a length out of range.
+// Prefix sums of the sequences' tiles into `pre` [B + 1] (shared memory), the number of shares into
+// pre[B + 1], the lengths behind them; block 0 also leaves all of it for the kernels that follow.  Lengths
+// are read here and nowhere else: were they changed meanwhile, the results would be wrong, but every
+// warp still walks the same units.  `scan` holds one value per warp.  Returns whether this thread met
+// a length out of range.
+__host__ __device__ constexpr size_t share_bytes(int64_t B) { return sizeof(uint32_t) * (size_t)((B + 3) / 2 * 2) + sizeof(int2) * (size_t)B; }
+__device__ __forceinline__ int2* share_lens(uint32_t* pre, int B) { return reinterpret_cast<int2*>(pre + (B + 3) / 2 * 2); }
+__device__ __forceinline__ const int2* share_lens(const uint32_t* pre, int B) { return reinterpret_cast<const int2*>(pre + (B + 3) / 2 * 2); }
+
 template <class U, int THREADS>
 __device__ __forceinline__ bool share_prefix(const AttendArgs& a, uint32_t* pre, uint64_t* scan)
 {
+    int2* len = share_lens(pre, a.B);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int run = (a.B + THREADS - 1) / THREADS, b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
     uint64_t mine = 0;  // units (high word) and tiles
@@ -122,6 +130,7 @@ __device__ __forceinline__ bool share_prefix(const AttendArgs& a, uint32_t* pre,
     for (int b = b0; b < b1; ++b) {
         const SeqLen s = seq_len(a, b);
         odd |= s.odd;
+        len[b] = make_int2(s.n, s.m);
         last = U::of_sequence(a, s);
         mine += last + ((uint64_t)(last ? a.c.heads * U::row_tiles(a, s.m) : 0) << 32);
     }
@@ -138,15 +147,17 @@ __device__ __forceinline__ bool share_prefix(const AttendArgs& a, uint32_t* pre,
     uint32_t at = (uint32_t)before;
     for (int b = b0; b < b1; ++b) {
         pre[b] = at;
-        at += b1 - b0 == 1 ? last : U::of_sequence(a, seq_len(a, b));
+        at += b1 - b0 == 1 ? last : U::of_sequence(a, SeqLen{len[b].x, len[b].y, false});
     }
     if (tid == THREADS - 1) {
         pre[a.B] = at;
         pre[a.B + 1] = share_count(at, (uint32_t)((before + mine) >> 32), gridDim.x);
     }
     __syncthreads();
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0) {
         for (int b = tid; b <= a.B + 1; b += THREADS) a.prefix[b] = pre[b];
+        for (int b = tid; b < a.B; b += THREADS) a.len[b] = len[b];
+    }
     return odd;
 }
 
@@ -166,7 +177,8 @@ __device__ __forceinline__ Segment segment_at(const AttendArgs& a, const uint32_
         if (pre[mid] <= w0) g.b = mid;
         else hi = mid;
     }
-    g.s = seq_len(a, g.b);
+    const int2 len = share_lens(pre, a.B)[g.b];
+    g.s = SeqLen{len.x, len.y, false};
     U::find(a, g.s, (pre[g.b + 1] - pre[g.b]) / a.c.heads, w0 - pre[g.b], g);
     g.t1 = min(g.tiles, g.t0 + (w1 - w0));
     return g;
@@ -186,19 +198,18 @@ __global__ void __launch_bounds__((kJoinThreads<D, U::R>)) kv8_join_kernel(const
     constexpr int JR = kJoinRows<U::R>, TPR = D / 4;
     const int jr = blockIdx.x % row_tiles_max, bh = blockIdx.x / row_tiles_max;
     const int h = bh % a.c.heads, b = bh / a.c.heads, rt = jr / (U::R / JR), sub = jr % (U::R / JR) * JR;
-    const SeqLen s = seq_len(a, b);
-    const bool rows = jr * JR < s.m * a.G;
+    after_me();
+    wait_before_me();  // in every block, so that this grid never ends before the one it joins
+    const int2 len = a.len[b];
+    const SeqLen s{len.x, len.y, false};
+    if (jr * JR >= s.m * a.G) return;
     __shared__ uint32_t s_tiles, s_before;
-    if (threadIdx.x == 0 && rows) {  // sums over row tiles: one thread's work
+    if (threadIdx.x == 0) {  // sums over row tiles: one thread's work
         s_tiles = U::tiles(a, s, rt);
         s_before = U::before(a, s, h, rt);
     }
     __syncthreads();
-    const uint32_t tiles = s_tiles, before = s_before;
-    after_me();
-    wait_before_me();  // in every block, so that this grid never ends before the one it joins
-    if (!rows) return;
-    const uint32_t W = a.prefix[a.B], w0 = a.prefix[b] + before, w1 = w0 + tiles;
+    const uint32_t tiles = s_tiles, W = a.prefix[a.B], w0 = a.prefix[b] + s_before, w1 = w0 + tiles;
     // the share that holds tile w: the smallest c with w < floor((c + 1) W / shares)
     const uint32_t shares = a.prefix[a.B + 1];
     const int c0 = tiles ? (int)(((uint64_t)(w0 + 1) * shares - 1) / W) : 0;

@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
 template <int D>
 cudaError_t launch_many(const AttendArgs& a, int grid, cudaStream_t st)
 {
-    const size_t smem = 1024 + sizeof(PrefillSmem<D>) + sizeof(uint32_t) * (size_t)(a.B + 2);
+    const size_t smem = 1024 + sizeof(PrefillSmem<D>) + share_bytes(a.B);
     cudaError_t e = cudaFuncSetAttribute(kv8_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kv8_prefill_kernel<D><<<grid, kThreadsP, smem, st>>>(a);
