@@ -54,6 +54,7 @@ struct F8Args {
     const float* sw;
     void* Y;
     int bf16, vec;
+    int box_m;  // rows of A's boxes: fewer than the tile's 128 where A has fewer (the rest of the stage is never stored)
     WsHeader* ws;
 };
 
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
                         alive = false;
                         break;
                     }
-                    mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(GM * GK + GN * GK));
+                    mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(a.box_m * GK + GN * GK));
                     tma_load_2d(sm.a[s], &tA, kb * GK, m0, &sm.full[s]);
                     tma_load_2d(sm.b[s], &tB, kb * GK, n0, &sm.full[s]);
                 }
@@ -716,7 +717,8 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
     DeviceGuard dev(A);
     if (!dev.ok) return HQ_ERR_ARG;
     const int64_t sms = num_sms(), mt = (M + GM - 1) / GM, kbs = (K + GK - 1) / GK, slabs = (N + GM - 1) / GM;
-    F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, static_cast<WsHeader*>(ws)};
+    F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, GM,
+             static_cast<WsHeader*>(ws)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CUtensorMap ta, tb;
     // few rows: as many parts of K as fill the SMs, in powers of two up to a portable cluster
@@ -730,12 +732,13 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
                                          : launch_gemm_fp8_few<64>(a, ta, tb, parts, st);
         return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
     }
-    const bool pair = ((M + 2 * GM - 1) / (2 * GM)) * ((N + PN - 1) / PN) >= sms / 2;
+    const bool pair = ((M + 2 * GM - 1) / (2 * GM)) * ((N + PN - 1) / PN) >= sms / 4;
     int gn = 128;  // the widest tile whose tiles occupy every SM, 32 columns if none does
     while (gn > 32 && mt * ((N + gn - 1) / gn) < sms) gn /= 2;
     // K blocks over all tiles of a CTA are counted in 31 bits
     if ((mt * ((N + gn - 1) / gn) / sms + 1) * ((K + GK - 1) / GK) > ((int64_t)1 << 30)) return HQ_ERR_UNSUPPORTED;
-    if (!tensor_map_bytes(&ta, A, M, K, lda, GM) || !tensor_map_bytes(&tb, W, N, K, ldw, pair ? GM : gn)) return HQ_ERR_CUDA;
+    if (!pair && M < GM) a.box_m = (int)((M + 7) / 8 * 8);
+    if (!tensor_map_bytes(&ta, A, M, K, lda, a.box_m) || !tensor_map_bytes(&tb, W, N, K, ldw, pair ? GM : gn)) return HQ_ERR_CUDA;
     const cudaError_t e = pair        ? launch_gemm_fp8_pair(a, ta, tb, st)
                           : gn == 128 ? launch_gemm_fp8<128>(a, ta, tb, st)
                                     : (gn == 64 ? launch_gemm_fp8<64>(a, ta, tb, st) : launch_gemm_fp8<32>(a, ta, tb, st));

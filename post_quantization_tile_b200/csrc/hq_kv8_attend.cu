@@ -513,7 +513,7 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The kernel for many rows (tensor memory, units of 256 rows) reads the cache once for all of them; this
 // one once for every sixteen, from L2.  One unit of sixteen rows: this one.
-bool many_rows(int64_t rows) { return rows > 16; }
+bool many_rows(int64_t rows) { return rows > 32; }
 constexpr int kMaxGridFew = 512, kMaxGridMany = 256;
 
 struct AttendLayout {
