@@ -394,7 +394,7 @@ hq_status_t hq_fp8_quantize(const void* x, hq_dtype_t dtype, int64_t rows, int64
  * between K and the pitch are not read), sa [ceil(K / 128), M], sw [ceil(K / 128), ceil(N / 128)] as
  * written by hq_fp8_quantize with block 1 and 128 (any finite scales are accepted), Y [M, N] bf16 or
  * fp32.  Every size from 1 up (K <= 2^20).  Block sums and the sum over blocks are binary32, in the
- * order of t; up to 64 rows, in up to eight parts of consecutive t whose sums are added in their order.
+ * order of t; up to sixteen rows, in up to eight parts of consecutive t whose sums are added in their order.
  * ws may be NULL; a bounded wait that ran out reports HQ_ERR_TIMEOUT there.
  */
 hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W, int64_t ldw,

@@ -467,16 +467,17 @@ cudaError_t launch_gemm_fp8_pair(const F8Args& a, const CUtensorMap& ta, const C
 }
 
 // ------------------------------------------------------------------------------------------------
-// The same product for few rows of A (M <= 64): bound by the bytes of W, which want many loads under way
-// on every SM from the first moment.  The weights take the MMA's 128 rows and A's rows its NT columns
-// (16, 32 or 64), and a cluster of up to eight CTAs divides the blocks of one 128-row slab of W, so that
+// The same product for up to sixteen rows of A and a long K: bound by the bytes of W, which want many loads
+// under way on every SM from the first moment.  The weights take the MMA's 128 rows and A's rows its NT
+// columns (16; with 32 and 64 the sums sent between CTAs made it slower than the tiles: 12.1 and 18.8 us
+// against 10.9 for 4096 x 4096), and a cluster of up to eight CTAs divides the blocks of one 128-row slab of W, so that
 // a 4096 x 4096 weight is one ring fill on 128 SMs.  Each CTA's scaled sums (binary32) meet over
 // distributed shared memory: CTA c of the cluster adds, in the order of the ranks, the columns
 // c NT / size .. of all of them and stores those.
 // ------------------------------------------------------------------------------------------------
 template <int NT>
 struct FewCfg {
-    static constexpr int STAGES = NT == 64 ? 7 : 8;
+    static constexpr int STAGES = 8;
     static constexpr int ACC = 256 / NT;  // accumulator slots in 256 TMEM columns
 };
 constexpr int kFewThreads = 192;  // producer, MMA issue, four epilogue warps
@@ -721,20 +722,26 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
              static_cast<WsHeader*>(ws)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CUtensorMap ta, tb;
-    // few rows: as many parts of K as fill the SMs, in powers of two up to a portable cluster
+    // A block of the tiled kernel takes about 0.25 us (a TMA round trip is hidden by the ring, the issue of its
+    // MMAs and commits is not) and half as much again at 128 columns; so the width with the fewest rounds of
+    // the SMs, weighed by that.  4096 columns and blocks of one row of tiles: 32 columns 11 us, 128: 19.
+    auto rounds = [&](int64_t width) { return (mt * ((N + width - 1) / width) + sms - 1) / sms; };
+    int gn = 128;
+    for (int w = 64; w >= 32; w /= 2)
+        if (rounds(w) * (128 + w) < rounds(gn) * (128 + gn)) gn = w;
+    // Up to sixteen rows: K in parts over a cluster, whose barriers cost about as much as fourteen blocks (3.5 us).
+    // 8 x 4096 x 4096: 8.7 us against 10.5 tiled; 8 x 11008 x 4096: 16.4, 22.8; 8 x 1024 x 4096: 7.1, 10.5; but
+    // 8 x 4096 x 2048: 7.4, 6.4; 8 x 1000 x 500: 6.3, 3.5.  Clusters of eight only where they leave half the
+    // SMs free (8 x 2048 x 2048 as 128 CTAs in eights: 11.4 us, twice the tiled time).
     int parts = 1;
-    while (parts < 8 && slabs * parts * 2 <= sms && kbs >= parts * 2) parts *= 2;
-    if (M <= 64 && slabs * parts <= kMaxSlots) {
-        const int nt = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
-        if (!tensor_map_bytes(&ta, A, M, K, lda, nt) || !tensor_map_bytes(&tb, W, N, K, ldw, GM)) return HQ_ERR_CUDA;
-        const cudaError_t e = nt == 16   ? launch_gemm_fp8_few<16>(a, ta, tb, parts, st)
-                              : nt == 32 ? launch_gemm_fp8_few<32>(a, ta, tb, parts, st)
-                                         : launch_gemm_fp8_few<64>(a, ta, tb, parts, st);
-        return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
+    while (parts < 8 && slabs * parts * 2 <= (parts == 4 ? sms / 2 : sms) && kbs >= parts * 2) parts *= 2;
+    if (M <= 16 && slabs * parts <= kMaxSlots && rounds(32) * kbs > kbs / parts + 14) {
+        if (!tensor_map_bytes(&ta, A, M, K, lda, 16) || !tensor_map_bytes(&tb, W, N, K, ldw, GM)) return HQ_ERR_CUDA;
+        return launch_gemm_fp8_few<16>(a, ta, tb, parts, st) == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
     }
+    // Pairs of CTAs from a quarter of the SMs' number of 256 x 256 tiles on: 48 tiles (768 x 4096 x 4096) 23.7 us
+    // against 28.2, 72 tiles 26.8 against 30.3, but 32 tiles (1024 x 2048 x 4096) 22.9 against 16.7.
     const bool pair = ((M + 2 * GM - 1) / (2 * GM)) * ((N + PN - 1) / PN) >= sms / 4;
-    int gn = 128;  // the widest tile whose tiles occupy every SM, 32 columns if none does
-    while (gn > 32 && mt * ((N + gn - 1) / gn) < sms) gn /= 2;
     // K blocks over all tiles of a CTA are counted in 31 bits
     if ((mt * ((N + gn - 1) / gn) / sms + 1) * ((K + GK - 1) / GK) > ((int64_t)1 << 30)) return HQ_ERR_UNSUPPORTED;
     if (!pair && M < GM) a.box_m = (int)((M + 7) / 8 * 8);

@@ -111,7 +111,7 @@ def test_gemm_ignores_the_padding_and_writes_in_place(hq):
 
 
 def test_gemm_rows_do_not_depend_on_the_batch(hq):
-    """Above 64 rows (where K is not divided) a row's result is the same whichever rows stand beside it."""
+    """Above sixteen rows (where K is not divided) a row's result is the same whichever rows stand beside it."""
     g = torch.Generator().manual_seed(4)
     w = codes(hq, g, 700, 900, 128)
     a = codes(hq, g, 600, 900, 1)
@@ -122,9 +122,9 @@ def test_gemm_rows_do_not_depend_on_the_batch(hq):
 
 
 @pytest.mark.parametrize("M", [1, 15, 16, 17, 32, 33, 63, 64, 65])
-@pytest.mark.parametrize("N,K_", [(128, 128), (200, 300), (1000, 2000), (20000, 256), (130, 20000)])
+@pytest.mark.parametrize("N,K_", [(128, 128), (200, 300), (1000, 2000), (20000, 256), (130, 20000), (4096, 4096), (1024, 4096), (11008, 2100)])
 def test_gemm_few_rows(hq, M, N, K_):
-    """Each width of the kernel for few rows, with K undivided and divided, more blocks than its ring holds."""
+    """Both sides of the rules for few rows: K undivided and divided, more blocks than a ring holds."""
     check_gemm(hq, M, N, K_, torch.float32)
 
 
