@@ -10,6 +10,10 @@
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 conversion, 12 MMA issue.
 //
+// 2 x 512 queries x 32 heads over 8192 slots: 177 us, 0.77 PFLOP/s, tensor pipe 37% and exponentials 38%
+// busy.  Bound by the chain of a step (scores out of TMEM, maximum, exponentials, P back, P V): with half of
+// the score MMAs, without the conversion or without the exponentials it stays at 167 to 175 us.
+//
 // Numerics as in the kernel for few rows (hq_kv8_attend.cu), except that value codes enter binary16
 // multiplied by their page's scale over the largest scale of the segment: exact for power-of-two
 // scales down to 2^-24 of that largest scale.
