@@ -134,10 +134,9 @@ __global__ void __launch_bounds__(kAThreads) kv8_append_kernel(const AppendArgs 
 // the weights once and finds the one that divides them digit by digit over order-preserving keys:
 // histograms of 11, 11 and 10 bits, each with a scan from the largest digit down.  Then every thread
 // takes a run of consecutive slots, counts, and writes its kept ones behind those of the threads before
-// it, so the kept slots come out in order.  Up to 8192 slots stay in registers (8 x 32 heads x 8192:
-// about 20 us, bound by instructions; from shared memory 26 us).
+// it, so the kept slots come out in order.  Up to 8192 slots stay in registers; bound by instructions and,
+// where half of the weights share an exponent, by the histogram's conflicts.
 // ------------------------------------------------------------------------------------------------
-constexpr int kEThreads = 1024;
 constexpr int kEBins = 2048;
 constexpr int64_t kEHeld = 40 * 1024;  // weights held in shared memory at most (160 KB)
 constexpr int64_t kEPages = 4096;      // pages whose first rows are held there, if a sequence has no more
@@ -177,42 +176,34 @@ __device__ __forceinline__ int64_t kept_len(const EvictArgs& a, int64_t b, bool&
     return max((int64_t)0, min(n, most));
 }
 
-// exclusive prefix sum of x over the thread block in thread order; `sums` holds one value per warp
-__device__ __forceinline__ uint64_t block_before(uint64_t x, uint64_t* sums)
+// exclusive prefix sum of x over the thread block in thread order; `sums` holds one value per warp and is
+// free again after the caller's next barrier
+__device__ __forceinline__ uint32_t block_before(uint32_t x, uint32_t* sums)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint64_t s = x;
+    uint32_t s = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t t = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, s, o);
         if (lane >= o) s += t;
     }
     if (lane == 31) sums[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-        uint64_t w = sums[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t t = __shfl_up_sync(0xFFFFFFFFu, w, o);
-            if (lane >= o) w += t;
-        }
-        sums[lane] = w;
-    }
-    __syncthreads();
-    return s - x + (warp ? sums[warp - 1] : 0ull);
+    return s - x + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sums[lane] : 0u);
 }
 
-// E > 0: up to E * 1024 weights, every thread's run of E consecutive ones in its registers; E = 0: any
-// number, from shared or global memory in every pass (the keys are made anew each time: five times the
-// instructions).
-template <int E>
-__global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a)
+// E > 0: up to E * T weights, every thread's run of E consecutive ones as keys in its registers (E divides
+// a page's sixteen slots, so the run lies on one page); E = 0: any number, from shared or global memory in
+// every pass (the keys are made anew each time).
+template <int T, int E>
+__global__ void __launch_bounds__(T, T == 512 ? 2 : 1) kv8_select_kernel(const EvictArgs a)
 {
+    constexpr int OWN = kEBins / T;  // bins of a thread
     extern __shared__ float held_w[];
     int32_t* held_row = reinterpret_cast<int32_t*>(held_w + a.held);
-    __shared__ uint32_t hist[kEBins];
+    __shared__ alignas(16) uint32_t hist[kEBins];
     __shared__ uint32_t s_digit, s_need;
-    __shared__ uint64_t sums[kEThreads / 32];
+    __shared__ uint32_t sums[2][32];
     const int h = blockIdx.x % a.c.heads;
     const int64_t b = blockIdx.x / a.c.heads;
     __shared__ int s_n;
@@ -220,6 +211,7 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
         bool odd;
         s_n = (int)kept_len(a, b, odd);
     }
+    for (int i = threadIdx.x; i < kEBins; i += T) hist[i] = 0u;
     __syncthreads();
     const int n = s_n, keep = (int)min((int64_t)n, a.budget);
     const float* w = a.w + b * a.wb + h * a.wh;
@@ -231,7 +223,7 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
         const int32_t id = __ldg(table + pg);
         return id >= 0 && id < a.c.pages ? (int)(((uint32_t)id * a.c.heads + h) << a.page_shift) : -1;
     };
-    for (int pg = threadIdx.x; pg < a.pages && pg << a.page_shift < n; pg += kEThreads) held_row[pg] = first_row(pg);
+    for (int pg = threadIdx.x; pg < a.pages && pg << a.page_shift < n; pg += T) held_row[pg] = first_row(pg);
     auto row_of = [&](int slot) {
         const int row = a.pages ? held_row[slot >> a.page_shift] : first_row(slot >> a.page_shift);
         return row < 0 ? -1 : row + (slot & (a.c.page - 1));
@@ -239,7 +231,7 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
     after_me();
     if (n <= a.budget) {
         __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kEThreads) {
+        for (int i = threadIdx.x; i < n; i += T) {
             idx[i] = row_of(i);
             if (out_w) out_w[i] = w[i];
         }
@@ -247,33 +239,28 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
     }
     const int recent = (int)min(a.recent, (int64_t)keep);
     const int old = n - recent, held = min(old, a.held);
-    const int run = E ? E : (old + kEThreads - 1) / kEThreads;
+    const int run = E ? E : (old + T - 1) / T;
     const int i0 = min(old, (int)threadIdx.x * run), i1 = min(old, i0 + run);
-    float mine_w[E ? E : 1];
     uint32_t mine_k[E ? E : 1];
+    if (E) {
+        float x[E ? E : 1];
+        if (E >= 4 && (reinterpret_cast<uintptr_t>(w) & 15u) == 0 && i0 + E <= i1) {
 #pragma unroll
-    for (int y = 0; y < E; ++y) mine_w[y] = i0 + y < i1 ? w[i0 + y] : 0.0f;
-    for (int i = threadIdx.x; i < kEBins; i += kEThreads) hist[i] = 0u;
-    if (E == 0) {
-#pragma unroll 4
-        for (int i = threadIdx.x; i < held; i += kEThreads) held_w[i] = w[i];
-    }
-#pragma unroll
-    for (int y = 0; y < E; ++y) mine_k[y] = weight_key(mine_w[y]);
-    auto weight_at = [&](int i) { return i < held ? held_w[i] : w[i]; };
-    // f(slot, key) over this thread's run, or (in any order) over a share of all slots
-    auto over_run = [&](auto f) {
-        if (E) {
-#pragma unroll
-            for (int y = 0; y < E; ++y)
-                if (i0 + y < i1) f(i0 + y, mine_k[y], mine_w[y]);
-        } else {
-            for (int i = i0; i < i1; ++i) {
-                const float x = weight_at(i);
-                f(i, weight_key(x), x);
+            for (int y = 0; y + 4 <= E; y += 4) {
+                const float4 four = *reinterpret_cast<const float4*>(w + i0 + y);
+                x[y] = four.x, x[y + 1] = four.y, x[y + 2] = four.z, x[y + 3] = four.w;
             }
+        } else {
+#pragma unroll
+            for (int y = 0; y < E; ++y) x[y] = i0 + y < i1 ? w[i0 + y] : 0.0f;
         }
-    };
+#pragma unroll
+        for (int y = 0; y < E; ++y) mine_k[y] = weight_key(x[y]);
+    } else {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < held; i += T) held_w[i] = w[i];
+    }
+    auto weight_at = [&](int i) { return i < held ? held_w[i] : w[i]; };
     uint32_t need = (uint32_t)(keep - recent);  // still to find at or below the digits fixed so far
     uint32_t key = 0xFFFFFFFFu;                 // need 0: nothing lies above, none is taken at it
     __syncthreads();
@@ -289,47 +276,72 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
                 for (int y = 0; y < E; ++y)
                     if (i0 + y < i1 && (mine_k[y] & mask) == key) atomicAdd(&hist[(mine_k[y] >> shift) & digits], 1u);
             } else {
-                for (int i = threadIdx.x; i < old; i += kEThreads) {
+                for (int i = threadIdx.x; i < old; i += T) {
                     const uint32_t k = weight_key(weight_at(i));
                     if ((k & mask) == key) atomicAdd(&hist[(k >> shift) & digits], 1u);
                 }
             }
             __syncthreads();
-            // thread t owns digits 2047 - 2 t and 2046 - 2 t: the scan runs from the largest down
-            const uint32_t d = kEBins - 1 - 2 * threadIdx.x, h0 = hist[d], h1 = hist[d - 1];
-            const uint32_t above = (uint32_t)block_before((uint64_t)(h0 + h1), sums);
-            if (above < need && need <= above + h0 + h1) {
-                const bool first = need <= above + h0;
-                s_digit = first ? d : d - 1;
-                s_need = need - above - (first ? 0u : h0);
+            // thread t owns the OWN digits from kEBins - 1 - OWN t down: the scan runs from the largest
+            const uint32_t low = kEBins - OWN * (threadIdx.x + 1);
+            uint32_t c[OWN], sum = 0;
+#pragma unroll
+            for (int y = 0; y < OWN; ++y) sum += c[y] = hist[low + y];
+            uint32_t above = block_before(sum, sums[0]);
+            if (above < need && need <= above + sum) {
+#pragma unroll
+                for (int y = OWN - 1; y >= 0; --y) {
+                    if (above < need && need <= above + c[y]) {
+                        s_digit = low + y;
+                        s_need = need - above;
+                    }
+                    above += c[y];
+                }
             }
-            hist[d] = 0u;
-            hist[d - 1] = 0u;
+#pragma unroll
+            for (int y = 0; y < OWN; ++y) hist[low + y] = 0u;
             __syncthreads();
             key |= s_digit << shift;
             mask |= digits << shift;
             need = s_need;
         }
     }
-    // counts of this thread's run: slots above the dividing key (high word), at it (low word)
+    // this thread's slots above the dividing key and at it
     uint32_t over = 0, same = 0;
-    over_run([&](int, uint32_t k, float) {
-        over += k > key;
-        same += k == key;
-    });
-    const uint64_t before = block_before(((uint64_t)over << 32) | same, sums);
-    uint32_t above = (uint32_t)(before >> 32), at = (uint32_t)before;
-    if (over | same)
-        over_run([&](int i, uint32_t k, float x) {
-            if (k > key || (k == key && at < need)) {
-                const uint32_t pos = above + min(at, need);
-                idx[pos] = row_of(i);
-                if (out_w) out_w[pos] = x;
-            }
-            above += k > key;
-            at += k == key;
-        });
-    for (int i = threadIdx.x; i < recent; i += kEThreads) {
+    if (E) {
+#pragma unroll
+        for (int y = 0; y < E; ++y) {
+            over += i0 + y < i1 && mine_k[y] > key;
+            same += i0 + y < i1 && mine_k[y] == key;
+        }
+    } else {
+        for (int i = i0; i < i1; ++i) {
+            const uint32_t k = weight_key(weight_at(i));
+            over += k > key;
+            same += k == key;
+        }
+    }
+    uint32_t above = block_before(over, sums[0]), at = block_before(same, sums[1]);
+    auto keep_slot = [&](int i, int row, uint32_t k) {
+        if (k > key || (k == key && at < need)) {
+            const uint32_t pos = above + min(at, need);
+            idx[pos] = row;
+            if (out_w) out_w[pos] = w[i];
+        }
+        above += k > key;
+        at += k == key;
+    };
+    if (over | same) {
+        if (E) {
+            const int row = row_of(i0);
+#pragma unroll
+            for (int y = 0; y < E; ++y)
+                if (i0 + y < i1) keep_slot(i0 + y, row < 0 ? -1 : row + y, mine_k[y]);
+        } else {
+            for (int i = i0; i < i1; ++i) keep_slot(i, row_of(i), weight_key(weight_at(i)));
+        }
+    }
+    for (int i = threadIdx.x; i < recent; i += T) {
         idx[keep - recent + i] = row_of(old + i);
         if (out_w) out_w[keep - recent + i] = w[old + i];
     }
@@ -338,8 +350,8 @@ __global__ void __launch_bounds__(kEThreads) kv8_select_kernel(const EvictArgs a
 // Second step: one thread block per (sequence, head, new page) gathers its rows of keys and values.  A page's
 // scale is the largest of its rows' old scales; a row with a smaller one is coded again.  Every thread
 // has all its 16-byte loads under way, beside the scales', before the first is stored.  Bound by the
-// scattered 64- or 128-byte rows: 8 x 32 heads, 2048 of 8192 slots, both steps 68 us, of which the selection
-// takes about 20; rows looked up one unit ahead made the registers cost residents (87 against 77 us then).
+// rows' bytes: 8 x 32 heads, 2048 of 8192 slots, 45 us of the operator's 63, 6.0 TB/s (91% of the copy rate);
+// rows looked up one unit ahead made the registers cost residents (87 against 77 us then).
 constexpr int kMThreads = 256;
 
 template <int D, int PASSES>
@@ -552,21 +564,28 @@ extern "C" hq_status_t hq_kv8_evict(const hq_kv8_evict_t* p, void* ws, size_t ws
     a.units = (uint32_t)(p->B * p->cache.heads * to_pages);
     a.page_shift = page_shift_of(p->cache.page);
     const int64_t most = p->L < p->max_pages * page ? p->L : p->max_pages * page;
-    const int runs = most <= kEThreads ? 1 : (most <= 4 * kEThreads ? 4 : (most <= 8 * kEThreads ? 8 : 0));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned blocks = (unsigned)(p->B * p->cache.heads);
+    // Weights in registers up to 8192.  Blocks of 1024 threads where every head has an SM of its own, else
+    // blocks of 512, two on an SM: 8 heads of 8192 slots 11.5 us (both steps) with 1024 threads, 13.4 with 512;
+    // 256 heads 50.6 and 47.7; 4000 slots 8.9, 9.6 and 24.1, 20.6.  Up to 1024 slots 512 threads either way:
+    // 6.8 against 7.1 us, 256 heads 10.6 against 13.9.  From shared memory: 16.0 and 56.5 at 8192 slots.
+    const bool wide = most > 1024 && blocks <= (unsigned)num_sms();
+    const int runs = most <= 1024 ? 2 : (most <= 4096 ? 8 : (most <= 8192 ? 16 : 0));  // of 512 threads
     a.held = runs ? 0 : (int)(most < kEHeld ? most : kEHeld);
     a.pages = p->max_pages <= kEPages ? (int)p->max_pages : 0;
     a.ws = static_cast<WsHeader*>(ws);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const size_t smem = 4 * (size_t)(a.held + a.pages);
-    const unsigned blocks = (unsigned)(p->B * p->cache.heads);
-    if (runs == 1) kv8_select_kernel<1><<<blocks, kEThreads, smem, st>>>(a);
-    else if (runs == 4) kv8_select_kernel<4><<<blocks, kEThreads, smem, st>>>(a);
-    else if (runs == 8) kv8_select_kernel<8><<<blocks, kEThreads, smem, st>>>(a);
+    if (runs == 2) kv8_select_kernel<512, 2><<<blocks, 512, smem, st>>>(a);
+    else if (runs == 8 && wide) kv8_select_kernel<1024, 4><<<blocks, 1024, smem, st>>>(a);
+    else if (runs == 8) kv8_select_kernel<512, 8><<<blocks, 512, smem, st>>>(a);
+    else if (runs == 16 && wide) kv8_select_kernel<1024, 8><<<blocks, 1024, smem, st>>>(a);
+    else if (runs == 16) kv8_select_kernel<512, 16><<<blocks, 512, smem, st>>>(a);
     else {
         // set on every call: the attribute belongs to the current device's context
-        if (cudaFuncSetAttribute(kv8_select_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(4 * (kEHeld + kEPages))) != cudaSuccess)
+        if (cudaFuncSetAttribute(kv8_select_kernel<1024, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(4 * (kEHeld + kEPages))) != cudaSuccess)
             return HQ_ERR_CUDA;
-        kv8_select_kernel<0><<<blocks, kEThreads, smem, st>>>(a);
+        kv8_select_kernel<1024, 0><<<blocks, 1024, smem, st>>>(a);
     }
     if (cudaGetLastError() != cudaSuccess) return HQ_ERR_CUDA;
     const int grid = slots_grid(a.units);

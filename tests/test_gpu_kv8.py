@@ -415,8 +415,15 @@ def test_evict_budgets(hq, n, budget, recent):
 
 @pytest.mark.parametrize("n,budget", [(1024, 500), (4096, 100), (4097, 2000), (8192, 8000), (8300, 4000), (45000, 300)])
 def test_evict_long_sequences(hq, n, budget):
-    """Weights in registers (runs of 1, 4, 8), in shared memory, and more than it holds."""
+    """Weights in registers (runs of 2, 4, 8), in shared memory, and more than it holds."""
     check_evict(hq, 1, 1, 64, 128, [n], budget, 7, seed=n)
+
+
+@pytest.mark.parametrize("n,budget", [(600, 599), (4000, 1000), (4097, 40)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_evict_many_heads(hq, n, budget, strided):
+    """More heads than multiprocessors; rows of weights on and off 16 bytes."""
+    check_evict(hq, 5, 40, 64, 128, [n, n - 1, 0, 17, n // 2 + 1], budget, min(13, budget), strided=strided, seed=n + 1)
 
 
 def test_evict_ties_zeros_signs_and_nan(hq):
