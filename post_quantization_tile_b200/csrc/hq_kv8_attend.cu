@@ -343,7 +343,10 @@ __global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
             ValueGroup<D> v;
             k.load(sm.ring[warp][stage][0]);
             v.load(sm.ring[warp][stage][1], end - tok);
-            __syncwarp();  // the stage is in registers: fill it again
+            // The stage is filled again by the asynchronous proxy, which does not wait for loads from shared
+            // memory that are merely issued: without the fence a group now and then read the next one's bytes.
+            fence_proxy_async();
+            __syncwarp();
             if (i + STAGES < count) issue(i + STAGES, stage);
             stage = stage + 1 == STAGES ? 0 : stage + 1;
             parity ^= stage == 0;

@@ -371,6 +371,27 @@ def test_append_bad_pages_and_full_tables(hq):
     check_append(hq, 2, 2, 4, 64, 16, [-3, 0], P=2, seed=24, status=7)
 
 
+def test_attend_repeats_bit_for_bit_on_a_long_cache(hq):
+    """A cache far larger than L2, so that loads land late and close together: every call the same bits."""
+    B, H, D, page, n = 8, 32, 128, 64, 4096
+    P = n // page
+    cache = hq.alloc_kv8(B * P, H, D, page)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for part in (cache.k, cache.v):
+        part.view(torch.uint8).copy_(torch.randint(0, 0x60, part.shape, generator=g, device="cuda", dtype=torch.uint8))
+    for scale in (cache.k_scale, cache.v_scale):
+        scale.fill_(2.0 ** -4)
+    table = torch.randperm(B * P, generator=g, device="cuda").to(torch.int32).view(B, P)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    q = torch.randn(B, H, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    outs = []
+    for _ in range(60):
+        out, lse = torch.empty_like(q), torch.empty(B, H, 1, device="cuda")
+        hq.kv8_attend(q, cache, table, lens, out=out, lse=lse)
+        outs.append((out, lse))
+    assert all(torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1]) for o, l in outs[1:])
+
+
 # ------------------------------------------------------------------------------------------------
 # evict
 # ------------------------------------------------------------------------------------------------
