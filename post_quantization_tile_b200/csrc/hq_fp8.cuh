@@ -115,7 +115,7 @@ struct Raw8<__nv_bfloat16> {
     __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
     __device__ __forceinline__ void load(const __nv_bfloat16* p)  // 16-byte aligned
     {
-        const uint4 x = __ldcs(reinterpret_cast<const uint4*>(p));
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
         w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     }
     __device__ __forceinline__ void load_part(const __nv_bfloat16* p, int64_t left)  // any alignment, `left` elements
@@ -147,7 +147,7 @@ struct Raw8<float> {
     }
     __device__ __forceinline__ void load(const float* p)
     {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
     __device__ __forceinline__ void load_part(const float* p, int64_t left)
