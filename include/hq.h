@@ -456,8 +456,8 @@ hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t ws_bytes, v
  *             NULL: 0; may be weights itself).  Slots behind are left as they were; slots j >= L are
  *             dropped (HQ_ERR_RANGE).
  *   ws        hq_kv8_attend_workspace_bytes(B, heads, Hq, Sq, dim, weights != NULL) bytes, 256-byte aligned
- * Products take bf16 queries and codes exactly and accumulate in binary32; probabilities enter the
- * second product as binary16.  B <= 2048.  The result does not depend on the other sequences' content.
+ * Products take bf16 queries (elements down to 2^-31 of a row's largest) and codes exactly, whatever the
+ * pages' scales, and accumulate in binary32; probabilities enter the second product as binary16.  B <= 2048.  The result does not depend on the other sequences' content.
  */
 typedef struct {
     hq_kv8_t cache;

@@ -10,15 +10,20 @@
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 conversion, 12 MMA issue.
 //
-// 2 x 512 queries x 32 heads over 8192 slots: 177 us, 0.77 PFLOP/s, tensor pipe 37% and exponentials 38%
+// 2 x 512 queries x 32 heads over 8192 slots: 182 us, 0.76 PFLOP/s, tensor pipe 37% and exponentials 38%
 // busy.  Bound by the chain of a step (scores out of TMEM, maximum, exponentials, P back, P V): with half of
 // the score MMAs, without the conversion or without the exponentials it stays at 167 to 175 us.
 //
-// Numerics as in the kernel for few rows (hq_kv8_attend.cu), except that value codes enter binary16
-// multiplied by their page's scale over the largest scale of the segment: exact for power-of-two
-// scales down to 2^-24 of that largest scale.
+// Numerics as in the kernel for few rows (hq_kv8_attend.cu).  One accumulator serves pages of unlike scales, so
+// value codes enter binary16 times 2^-15 .. 2^7, their page's scale (up to the next power of two) over the
+// accumulator's unit: exact, since the last bit of e4m3 is 2^-9, of binary16 2^-24.  A segment whose pages' value
+// scales span more than these 22 octaves is walked once for each window of 22, the quietest first, with the
+// values outside the window as zeros and the accumulator brought to the next window's unit in between; four
+// windows hold 2^-40 .. 2^40.  What a scale lacks to a power of two multiplies the probabilities of its slots.
 #include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "hq_kv8_attend.cuh"
 #include "hq_tc.cuh"
@@ -30,6 +35,12 @@ constexpr int kThreadsP = 512;
 constexpr int kTok = 128;     // slots of a tile
 constexpr int kStep = 64;     // slots of one step of the softmax: a row tile has two buffers of scores
 constexpr int kScaleRing = 4;  // tiles whose key scales are kept: the converter is at most two ahead
+constexpr int kWindows = 4;    // value scales: windows of a segment at most
+constexpr float kWindow = 4194304.0f, kWindowTop = 128.0f;  // their width, and their largest scale over the unit
+
+// the power of two at or above a positive scale, and the reciprocal of a power of two
+__device__ __forceinline__ float pow2_above(float x) { return __uint_as_float((__float_as_uint(x) + 0x7FFFFFu) & 0x7F800000u); }
+__device__ __forceinline__ float pow2_inverse(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 
 // units of 256 rows; a unit's tiles end with the last slot that any of its rows sees
 struct ManyRows {
@@ -74,8 +85,12 @@ struct PrefillSmem {
     alignas(1024) unsigned char k[2][D / 64][HALF];
     alignas(1024) unsigned char v[2][D / 64][HALF];
     alignas(16) float ks[kScaleRing][8];  // key scale of each sixteen slots; negative: no such page
-    float vref[4];                        // by segment
-    float red[4];
+    alignas(16) float vm[kScaleRing][8];  // their value scale over the power of two above it
+    int2 seg[4];                          // by segment: windows, whether a value scale is no power of two
+    float vref[4];                        // by window: the accumulator's unit
+    float cut[kWindows + 1], top[kWindows];  // the converter's: a segment's windows (cut[i], cut[i + 1]], their largest scales
+    alignas(16) uint32_t red[4][4];
+    float sum[256];                       // by row: the first window's
     alignas(8) uint64_t k_full[2];
     uint64_t k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2][2], p_ready[2][2];  // by row tile and score buffer
@@ -106,6 +121,21 @@ __device__ __forceinline__ void put_codes(unsigned char* run, int row, int c, ui
         }
     *reinterpret_cast<uint4*>(run + swz(row, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
     *reinterpret_cast<uint4*>(run + swz(row, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// this thread's row of an accumulator times f
+template <int D>
+__device__ __forceinline__ void scale_row(uint32_t to, float f)
+{
+#pragma unroll 1
+    for (int p = 0; p < D / 32; ++p) {
+        uint32_t o[32];
+        tmem_ld32_nowait(to + 32 * p, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+        tmem_st32(to + 32 * p, o);
+    }
 }
 
 template <int D>
@@ -159,7 +189,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lanes + 128 * t, to = lanes + 256 + 128 * t;
-        uint32_t seg_n = 0, tile_n = 0, s_n = 0, pv_n = 0;  // segments and slot tiles, and those and the steps of this row tile
+        // segments, windows and slot tiles, and those and the steps of this row tile
+        uint32_t seg_n = 0, win_n = 0, tile_n = 0, s_n = 0, pv_n = 0;
         while (w0 < w1) {
             const Segment g = segment_at<ManyRows>(a, pre, w0, w1);
             const int row = g.rt * kManyRows + t * 128 + r, i = row / a.G;
@@ -195,86 +226,110 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_ready[t]);
             const int full_end = (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)end);
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f, vref = 1.0f;
             const int T = (int)(g.t1 - g.t0);
+            int windows = 1;
             if (active) {
 #pragma unroll 1
-                for (int i2 = 0; i2 < 2 * T; ++i2) {
-                    const int tok = (int)g.t0 * kTok + i2 * kStep, buf = i2 & 1;
-                    const uint32_t tb = ts + kStep * buf;
-                    wait(&sm.s_full[t][buf], s_n + (i2 >> 1));
-                    if (!alive) continue;
-                    tc_fence_after();
-                    uint32_t S[2][32];
-                    tmem_ld32_nowait(tb, S[0]);
-                    tmem_ld32_nowait(tb + 32, S[1]);
-                    const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[(tile_n + (i2 >> 1)) % kScaleRing][4 * buf]);
-                    tmem_wait_ld();
-                    if (tok + kStep > full_end || fminf(fminf(ks.x, ks.y), fminf(ks.z, ks.w)) < 0.0f) {
-                        // slots that some row does not see, or whose page is missing
-                        const int left = end - tok;
-#pragma unroll
-                        for (int y = 0; y < kStep; ++y)
-                            if (y >= left || (y < 16 ? ks.x : (y < 32 ? ks.y : (y < 48 ? ks.z : ks.w))) < 0.0f) S[y >> 5][y & 31] = 0xFF800000u;
+                for (int win = 0; win < windows; ++win) {
+                    bool odd = false;
+                    wait(&sm.s_full[t][0], s_n);  // the window's first scores, and with them what the converter says of it
+                    if (alive) {
+                        const int2 of_seg = sm.seg[seg_n & 3];
+                        const float unit = sm.vref[win_n & 3];
+                        windows = of_seg.x;
+                        odd = of_seg.y != 0;
+                        if (win > 0) {
+                            wait(&sm.pv_done[t], pv_n - 1);
+                            tc_fence_after();
+                            if (alive) scale_row<D>(to, vref / unit);
+                        }
+                        vref = unit;
                     }
-                    const float cg[4] = {c * fabsf(ks.x), c * fabsf(ks.y), c * fabsf(ks.z), c * fabsf(ks.w)};
-                    float x[8];
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) x[z] = __uint_as_float(S[z >> 2][(z & 3) * 8]);
-#pragma unroll
-                    for (int y = 1; y < 8; ++y)
-#pragma unroll
-                        for (int z = 0; z < 8; ++z) x[z] = fmaxf(x[z], __uint_as_float(S[z >> 2][(z & 3) * 8 + y]));
-                    const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]) * cg[0], fmaxf(x[2], x[3]) * cg[1]),
-                                            fmaxf(fmaxf(x[4], x[5]) * cg[2], fmaxf(x[6], x[7]) * cg[3]));
-                    const bool moves = top > m + kSlack;
-                    if (__any_sync(0xFFFFFFFFu, moves)) {
-                        const float next = moves ? top : m, f = m == -INFINITY ? 1.0f : ex2(m - next);
-                        l *= f;
-                        m = next;
-                        if (i2 > 0) {  // once the products before this step's are done
-                            wait(&sm.pv_done[t], pv_n + i2 - 1);
+                    ++win_n;
+                    auto steps = [&](auto with_factors) {
+                        constexpr bool ODD = decltype(with_factors)::value;
+#pragma unroll 1
+                        for (int i2 = 0; i2 < 2 * T; ++i2) {
+                            const int tok = (int)g.t0 * kTok + i2 * kStep, buf = i2 & 1;
+                            const uint32_t tb = ts + kStep * buf;
+                            wait(&sm.s_full[t][buf], s_n + (i2 >> 1));
                             if (!alive) continue;
                             tc_fence_after();
-#pragma unroll 1
-                            for (int p = 0; p < D / 32; ++p) {
-                                uint32_t o[32];
-                                tmem_ld32_nowait(to + 32 * p, o);
-                                tmem_wait_ld();
+                            uint32_t S[2][32];
+                            tmem_ld32_nowait(tb, S[0]);
+                            tmem_ld32_nowait(tb + 32, S[1]);
+                            const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[(tile_n + (i2 >> 1)) % kScaleRing][4 * buf]);
+                            tmem_wait_ld();
+                            if (tok + kStep > full_end || fminf(fminf(ks.x, ks.y), fminf(ks.z, ks.w)) < 0.0f) {
+                                // slots that some row does not see, or whose page is missing
+                                const int left = end - tok;
 #pragma unroll
-                                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                                tmem_st32(to + 32 * p, o);
+                                for (int y = 0; y < kStep; ++y)
+                                    if (y >= left || (y < 16 ? ks.x : (y < 32 ? ks.y : (y < 48 ? ks.z : ks.w))) < 0.0f) S[y >> 5][y & 31] = 0xFF800000u;
                             }
-                        }
-                    }
-                    const float sub = m == -INFINITY ? 0.0f : m - kBoost;
-                    const float2 nsub = make_float2(-sub, -sub);
-                    float2 sum = make_float2(0.0f, 0.0f);
+                            const float cg[4] = {c * fabsf(ks.x), c * fabsf(ks.y), c * fabsf(ks.z), c * fabsf(ks.w)};
+                            float x[8];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t P[16];
+                            for (int z = 0; z < 8; ++z) x[z] = __uint_as_float(S[z >> 2][(z & 3) * 8]);
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            const float cq = cg[2 * p + (y >> 3)];
-                            float2 e = __ffma2_rn(make_float2(__uint_as_float(S[p][2 * y]), __uint_as_float(S[p][2 * y + 1])),
-                                                  make_float2(cq, cq), nsub);
-                            e = make_float2(ex2(e.x), ex2(e.y));
-                            sum = f2add(sum, e);
-                            P[y] = pack_f16(e.x, e.y);
+                            for (int y = 1; y < 8; ++y)
+#pragma unroll
+                                for (int z = 0; z < 8; ++z) x[z] = fmaxf(x[z], __uint_as_float(S[z >> 2][(z & 3) * 8 + y]));
+                            const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]) * cg[0], fmaxf(x[2], x[3]) * cg[1]),
+                                                    fmaxf(fmaxf(x[4], x[5]) * cg[2], fmaxf(x[6], x[7]) * cg[3]));
+                            const bool moves = top > m + kSlack;
+                            if (__any_sync(0xFFFFFFFFu, moves)) {  // in the first window only: the others see the same scores
+                                const float next = moves ? top : m, f = m == -INFINITY ? 1.0f : ex2(m - next);
+                                l *= f;
+                                m = next;
+                                if (i2 > 0) {  // once the products before this step's are done
+                                    wait(&sm.pv_done[t], pv_n + i2 - 1);
+                                    if (!alive) continue;
+                                    tc_fence_after();
+                                    scale_row<D>(to, f);
+                                }
+                            }
+                            const float sub = m == -INFINITY ? 0.0f : m - kBoost;
+                            const float2 nsub = make_float2(-sub, -sub);
+                            float2 sum = make_float2(0.0f, 0.0f);
+                            const float4 vm = ODD ? *reinterpret_cast<const float4*>(&sm.vm[(tile_n + (i2 >> 1)) % kScaleRing][4 * buf])
+                                                  : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                            const float vg[4] = {vm.x, vm.y, vm.z, vm.w};
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+                                uint32_t P[16];
+#pragma unroll
+                                for (int y = 0; y < 16; ++y) {
+                                    const float cq = cg[2 * p + (y >> 3)];
+                                    float2 e = __ffma2_rn(make_float2(__uint_as_float(S[p][2 * y]), __uint_as_float(S[p][2 * y + 1])),
+                                                          make_float2(cq, cq), nsub);
+                                    e = make_float2(ex2(e.x), ex2(e.y));
+                                    sum = f2add(sum, e);
+                                    if (ODD) e = f2mul(e, make_float2(vg[2 * p + (y >> 3)], vg[2 * p + (y >> 3)]));
+                                    P[y] = pack_f16(e.x, e.y);
+                                }
+                                tmem_st16(tb + 16 * p, P);
+                            }
+                            l += sum.x + sum.y;
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.p_ready[t][buf]);
                         }
-                        tmem_st16(tb + 16 * p, P);
-                    }
-                    l += sum.x + sum.y;
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_ready[t][buf]);
+                    };
+                    if (odd) steps(std::true_type{});
+                    else steps(std::false_type{});
+                    if (win == 0 && windows > 1) sm.sum[tid] = l;
+                    s_n += T;
+                    pv_n += 2 * T;
+                    tile_n += T;
                 }
+                if (windows > 1) l = sm.sum[tid];  // once for all windows
                 // the segment's accumulator
                 wait(&sm.o_full[t], seg_n);
                 if (alive) {
                     tc_fence_after();
-                    const float vref = sm.vref[seg_n & 3];
                     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
                     const int slot = 2 * blockIdx.x + (g.t0 == 0 ? 1 : 0);
                     const float f = whole ? (l == 0.0f ? 0.0f : vref / l) : vref;
@@ -313,12 +368,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     }
                     tc_fence_before();
                 }
-                s_n += T;
-                pv_n += 2 * T;
             } else {
                 wait(&sm.o_full[t], seg_n);  // without rows: keep step with the others, one segment at a time
+                if (alive) windows = sm.seg[seg_n & 3].x;
+                win_n += windows;
+                tile_n += T * windows;
             }
-            tile_n += T;
             ++seg_n;
             w0 += T;
         }
@@ -327,24 +382,63 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
         // a pass: 32 rows by 64 dims; a warp's eight rows lie in one group of sixteen slots
         constexpr int RUNS = D / 64, PASSES = 4 * RUNS;
         const int ct = tid - 256, c = ct & 3, row0 = ct >> 2, half = ct >> 6;
-        uint32_t seg_n = 0, tile_n = 0;
+        uint32_t seg_n = 0, win_n = 0, tile_n = 0;
         while (w0 < w1) {
             const Segment g = segment_at<ManyRows>(a, pre, w0, w1);
             const int32_t* table = a.table + g.b * a.table_stride;
             const int end = min((int)g.t1 * kTok, ManyRows::end(a, g.s, g.rt)), T = (int)(g.t1 - g.t0);
-            // the largest value scale of the segment's pages
-            float vmax = 0.0f;
-            for (int tok = ((int)g.t0 * kTok / a.c.page + ct) * a.c.page; tok < end; tok += 128 * a.c.page) {
-                const int32_t id = __ldg(table + (tok >> a.page_shift));
-                if (id >= 0 && id < a.c.pages) vmax = fmaxf(vmax, __ldg(a.c.v_scale + (int64_t)id * a.c.heads + g.h));
-                else atomicOr(&sm.status, kStRange);
+            // of the value scales of the segment's pages: the largest up to `cut`, the smallest above it, the
+            // largest of all, and whether one is no power of two (positive floats order like their bit patterns)
+            auto scales = [&](float cut, float& under, float& above, float& top) {
+                uint32_t u = 0u, o = 0x7F800000u, m = 0u, odd = 0u;
+                for (int tok = ((int)g.t0 * kTok / a.c.page + ct) * a.c.page; tok < end; tok += 128 * a.c.page) {
+                    const int32_t id = __ldg(table + (tok >> a.page_shift));
+                    if (id >= 0 && id < a.c.pages) {
+                        const float vs = __ldg(a.c.v_scale + (int64_t)id * a.c.heads + g.h);
+                        const uint32_t w = __float_as_uint(vs);
+                        if (!(vs > 0.0f)) continue;
+                        if (vs > cut) o = min(o, w);
+                        else u = max(u, w);
+                        m = max(m, w);
+                        odd |= w & 0x7FFFFFu;
+                    } else {
+                        atomicOr(&sm.status, kStRange);
+                    }
+                }
+                u = __reduce_max_sync(0xFFFFFFFFu, u);
+                o = __reduce_min_sync(0xFFFFFFFFu, o);
+                m = __reduce_max_sync(0xFFFFFFFFu, m);
+                odd = __reduce_or_sync(0xFFFFFFFFu, odd);
+                named_sync(1, 128);  // what the last call left is read
+                if (lane == 0) *reinterpret_cast<uint4*>(sm.red[warp - 8]) = make_uint4(u, o, m, odd);
+                named_sync(1, 128);
+                for (int w = 0; w < 4; ++w) {
+                    u = max(u, sm.red[w][0]);
+                    o = min(o, sm.red[w][1]);
+                    m = max(m, sm.red[w][2]);
+                    odd |= sm.red[w][3];
+                }
+                under = __uint_as_float(u);
+                above = __uint_as_float(o);
+                top = __uint_as_float(m);
+                return odd != 0u;
+            };
+            float under, low, vmax, cut_lo = 0.0f, cut_hi = INFINITY;
+            const bool odd = scales(0.0f, under, low, vmax);
+            int windows = 1;
+            if (vmax > low * kWindow) {
+                float from = 0.0f;
+                for (windows = 0; windows < kWindows; ++windows) {
+                    const bool last = windows == kWindows - 1 || vmax <= low * kWindow;
+                    const float to = last ? INFINITY : low * kWindow;
+                    if (!last) scales(to, under, low, vmax);
+                    if (ct == 0) sm.cut[windows] = from, sm.cut[windows + 1] = to, sm.top[windows] = last ? vmax : under;
+                    from = to;
+                    if (last) break;
+                }
+                ++windows;
+                named_sync(1, 128);
             }
-            vmax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vmax)));
-            named_sync(1, 128);  // the last segment's maximum is read
-            if (lane == 0) sm.red[warp - 8] = vmax;
-            named_sync(1, 128);
-            vmax = fmaxf(fmaxf(sm.red[0], sm.red[1]), fmaxf(sm.red[2], sm.red[3]));
-            const float vref = vmax > 0.0f ? vmax : 1.0f;
             // the groups of sixteen slots of a tile: lane y < 8 knows the page (two tiles ahead of the codes),
             // the first cache row and the scales (one ahead) of group y; the keys of the next tile and the
             // values of this one are on their way while the tile before is stored
@@ -372,44 +466,50 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                 }
             };
             uint4 xk[PASSES], xv[PASSES];
-            find_pages(0);
-            find_rows(0);
-            find_pages(1);
-            fetch(xk, a.c.k);
 #pragma unroll 1
-            for (int j = 0; j < T; ++j, ++tile_n) {
-                const int st = tile_n & 1;
-                fetch(xv, a.c.v);
-                const float ks = g_scale.x, vr = g_scale.y / vref;
-                const uint32_t vr2 = pack_f16(vr, vr);
-                // values that nobody may see are zeros: behind the last slot, and of missing pages
-                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, g_row < 0) & 0xFFu;
-                const bool edge = gone != 0u || tok0 + (j + 1) * kTok > end;
-                find_rows(j + 1);
-                find_pages(j + 2);
-                if (tile_n >= 2) wait(&sm.k_empty[st], tile_n / 2 - 1);
-                if (ct < 8) sm.ks[tile_n % kScaleRing][ct] = ks;
-                if (ct == 0 && j == 0) sm.vref[seg_n & 3] = vref;
-#pragma unroll
-                for (int p = 0; p < PASSES; ++p) put_codes<false>(sm.k[st][p % RUNS], (p / RUNS) * 32 + row0, c, xk[p], 0u);
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.k_full[st]);
+            for (int win = 0; win < windows; ++win, ++win_n) {
+                if (windows > 1) cut_lo = sm.cut[win], cut_hi = sm.cut[win + 1], vmax = sm.top[win];
+                const float vref = vmax > 0.0f ? pow2_above(vmax) * (1.0f / kWindowTop) : 1.0f, inv = pow2_inverse(vref);
+                find_pages(0);
+                find_rows(0);
+                find_pages(1);
                 fetch(xk, a.c.k);
-                if (tile_n >= 2) wait(&sm.v_empty[st], tile_n / 2 - 1);
-                if (edge)
+#pragma unroll 1
+                for (int j = 0; j < T; ++j, ++tile_n) {
+                    const int st = tile_n & 1;
+                    fetch(xv, a.c.v);
+                    const float ks = g_scale.x, v2 = pow2_above(g_scale.y), vm = g_scale.y * pow2_inverse(v2);
+                    const float vr = g_scale.y > cut_lo && g_scale.y <= cut_hi ? v2 * inv : 0.0f;
+                    const uint32_t vr2 = pack_f16(vr, vr);
+                    // values that nobody may see are zeros: behind the last slot, and of missing pages
+                    const uint32_t gone = __ballot_sync(0xFFFFFFFFu, g_row < 0) & 0xFFu;
+                    const bool edge = gone != 0u || tok0 + (j + 1) * kTok > end;
+                    find_rows(j + 1);
+                    find_pages(j + 2);
+                    if (tile_n >= 2) wait(&sm.k_empty[st], tile_n / 2 - 1);
+                    if (ct < 8) sm.ks[tile_n % kScaleRing][ct] = ks, sm.vm[tile_n % kScaleRing][ct] = vm;
+                    if (ct == 0 && j == 0) sm.seg[seg_n & 3] = make_int2(windows, odd), sm.vref[win_n & 3] = vref;
 #pragma unroll
-                    for (int p = 0; p < PASSES; ++p) {
-                        const int r = (p / RUNS) * 32 + row0;
-                        if ((gone >> (r >> 4) & 1u) || tok0 + j * kTok + r >= end) xv[p] = make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    for (int p = 0; p < PASSES; ++p) put_codes<false>(sm.k[st][p % RUNS], (p / RUNS) * 32 + row0, c, xk[p], 0u);
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.k_full[st]);
+                    fetch(xk, a.c.k);
+                    if (tile_n >= 2) wait(&sm.v_empty[st], tile_n / 2 - 1);
+                    if (edge)
 #pragma unroll
-                for (int p = 0; p < PASSES; ++p)
-                    put_codes<true>(sm.v[st][p % RUNS], (p / RUNS) * 32 + row0, c, xv[p],
-                                    __shfl_sync(0xFFFFFFFFu, vr2, 2 * (p / RUNS) + half));
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.v_full[st]);
+                        for (int p = 0; p < PASSES; ++p) {
+                            const int r = (p / RUNS) * 32 + row0;
+                            if ((gone >> (r >> 4) & 1u) || tok0 + j * kTok + r >= end) xv[p] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+#pragma unroll
+                    for (int p = 0; p < PASSES; ++p)
+                        put_codes<true>(sm.v[st][p % RUNS], (p / RUNS) * 32 + row0, c, xv[p],
+                                        __shfl_sync(0xFFFFFFFFu, vr2, 2 * (p / RUNS) + half));
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.v_full[st]);
+                }
             }
             ++seg_n;
             w0 += T;
@@ -440,6 +540,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                 wait(&sm.q_ready[1], seg_n);
                 wait(&sm.k_full[tile_n & 1], tile_n / 2);
                 tc_fence_after();
+                const int tiles = T * (alive ? __shfl_sync(0xFFFFFFFFu, sm.seg[seg_n & 3].x, 0) : 1);  // of all windows
                 if (alive) {
 #pragma unroll
                     for (int buf = 0; buf < 2; ++buf)
@@ -449,10 +550,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     mma_commit_warp(&sm.k_empty[tile_n & 1], leader);
                 }
 #pragma unroll 1
-                for (int j = 0; j < T; ++j, ++tile_n) {
+                for (int j = 0; j < tiles; ++j, ++tile_n) {
                     const int st = tile_n & 1, next = st ^ 1;
                     wait(&sm.v_full[st], tile_n / 2);
-                    if (j + 1 < T) wait(&sm.k_full[next], (tile_n + 1) / 2);
+                    if (j + 1 < tiles) wait(&sm.k_full[next], (tile_n + 1) / 2);
 #pragma unroll
                     for (int buf = 0; buf < 2; ++buf)
 #pragma unroll
@@ -467,7 +568,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                                            dv + (st ? TILE : 0) + (buf ? HALFTILE : 0) + (uint64_t)(128 * kk), IDO, j > 0 || buf > 0 || kk > 0, leader);
                             mma_commit_warp(&sm.pv_done[t], leader);
                             if (buf && t == nt - 1) mma_commit_warp(&sm.v_empty[st], leader);
-                            if (j + 1 < T) {  // the scores of two steps on take this step's buffer
+                            if (j + 1 < tiles) {  // the scores of two steps on take this step's buffer
                                 score(t, next, buf);
                                 if (buf && t == nt - 1) mma_commit_warp(&sm.k_empty[next], leader);
                             } else if (buf) {
