@@ -209,10 +209,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                     for (int y = 0; y < 4; ++y) top = max(top, max((w[y] << 16) & 0x7FFF0000u, w[y] & 0x7FFF0000u));
                 }
                 // a power of two brings the row's largest to [2^14, 2^15); a negative scale goes into the
-                // queries, a zero one becomes tiny, so that the factors of the scores are positive
+                // queries, so that the factors of the scores are not negative
                 const int e = top ? min(126, 14 + 127 - (int)(top >> 23)) : 0;
                 const float up = a.scale < 0.0f ? -exp2_int(e) : exp2_int(e);
-                c = fmaxf(exp2_int(-e) * fabsf(a.scale) * kLog2e, 1e-37f);
+                c = exp2_int(-e) * fabsf(a.scale) * kLog2e;
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j) {
                     const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
@@ -268,7 +268,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) kv8_prefill_kernel(const AttendA
                                 for (int y = 0; y < kStep; ++y)
                                     if (y >= left || (y < 16 ? ks.x : (y < 32 ? ks.y : (y < 48 ? ks.z : ks.w))) < 0.0f) S[y >> 5][y & 31] = 0xFF800000u;
                             }
-                            const float cg[4] = {c * fabsf(ks.x), c * fabsf(ks.y), c * fabsf(ks.z), c * fabsf(ks.w)};
+                            // the scores' factors, positive: a masked score times zero would be NaN (products of codes
+                            // and queries stay below 2^31, so that scores times 1e-30 are zeros all the same)
+                            const float cg[4] = {fmaxf(c * fabsf(ks.x), 1e-30f), fmaxf(c * fabsf(ks.y), 1e-30f),
+                                                 fmaxf(c * fabsf(ks.z), 1e-30f), fmaxf(c * fabsf(ks.w), 1e-30f)};
                             float x[8];
 #pragma unroll
                             for (int z = 0; z < 8; ++z) x[z] = __uint_as_float(S[z >> 2][(z & 3) * 8]);

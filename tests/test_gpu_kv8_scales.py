@@ -116,3 +116,14 @@ def test_scales_that_are_no_powers_of_two(hq, rows, causal):
     cache, table = make(hq, 5, 10, 32, 128, k_exp=np.linspace(-9.7, -8.1, 10), v_exp=np.linspace(-11.3, 9.9, 10))
     check(hq, cache, table, 310, queries(rows, 1, rows, 128), causal=causal)
     check(hq, cache, table, 1, queries(rows, 1, rows, 128), causal=causal)  # one slot: its values come back
+
+
+@pytest.mark.parametrize("k_exp", [-40, -27, 0])
+@pytest.mark.parametrize("rows", ROWS)
+def test_scores_whose_factor_vanishes_in_binary32(hq, rows, k_exp):
+    """scale 0, tiny scales and tiny queries against pages of tiny (or zero) keys that a causal row sees in part."""
+    cache, table = make(hq, 7, 6, 64, 64, k_exp=[k_exp] * 6)
+    for scale, up in ((0.0, 1.0), (-0.0, 1.0), (1e-38, 1.0), (0.125, 2.0 ** -100), (0.125, 0.0), (-0.125, 2.0 ** -126)):
+        q = (queries(rows, 1, rows, 64).float() * up).to(torch.bfloat16)
+        check(hq, cache, table, 333, q, scale=scale, weights=True)
+        cache.k.view(torch.uint8)[int(table[0, 4])] = 0
