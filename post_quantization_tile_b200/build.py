@@ -29,7 +29,7 @@ SOURCES = ["hq_api.cu", "hq_noalloc.cu", "hq_gemm.cu", "hq_gemm_code.cu", "hq_de
            "hq_gemm_fp8.cu", "hq_kv8.cu", "hq_kv8_attend.cu", "hq_kv8_prefill.cu", "hq_inst_z.cu", "hq_inst_a2.cu", "hq_inst_d4.cu",
            "hq_inst_e8.cu"]
 # sources compiled a second time with the test hooks for libhq_test.so
-TEST_SOURCES = ["hq_api.cu", "hq_inst_e8.cu"]
+TEST_SOURCES = ["hq_api.cu", "hq_inst_e8.cu", "hq_gemm_fp8.cu"]
 HEADERS = ["hq_common.cuh", "hq_tc.cuh", "hq_lattice.cuh", "hq_encode.cuh", "hq_decode.cuh", "hq_instantiate.cuh", "hq_launch.h",
            "hq_fp8.cuh", "hq_kv8.cuh", "hq_kv8_attend.cuh"]
 

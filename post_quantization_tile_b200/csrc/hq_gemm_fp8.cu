@@ -24,6 +24,9 @@
 #include "hq_fp8.cuh"
 #include "hq_launch.h"
 #include "hq_tc.cuh"
+#ifdef HQ_TEST_HOOKS
+#include "../../include/hq_test.h"
+#endif
 
 namespace hq {
 namespace {
@@ -60,7 +63,37 @@ struct F8Args {
     int bf16, vec;
     int box_m;  // rows of A's boxes: fewer than the tile's 128 where A has fewer (the rest of the stage is never stored)
     WsHeader* ws;
+    // read only by the test build (HQ_TEST_HOOKS): the block of every CTA whose MMAs are withheld, so that the
+    // waits behind it run out, and two words a CTA, boxes asked for and boxes awaited at the end
+    int test_silent;
+    uint32_t* test_log;
 };
+
+__device__ __forceinline__ bool test_withheld(const F8Args& a, int it)
+{
+#ifdef HQ_TEST_HOOKS
+    return it == a.test_silent;
+#else
+    return false;
+#endif
+}
+__device__ __forceinline__ void test_boxes(const F8Args& a, int issued, int awaited)
+{
+#ifdef HQ_TEST_HOOKS
+    a.test_log[2 * blockIdx.x] = issued;
+    a.test_log[2 * blockIdx.x + 1] = awaited;
+#endif
+}
+
+// No copy may be in flight when a block leaves, whatever ended its work: waits for the last boxes of a ring
+// of which `issued` were asked for.
+template <int STAGES>
+__device__ __forceinline__ void await_boxes(const F8Args& a, uint64_t* full, int issued)
+{
+    int landed = 0;
+    for (int it = max(0, issued - STAGES); it < issued; ++it) landed += mbar_wait_sleep(&full[it % STAGES], (uint32_t)((it / STAGES) & 1));
+    test_boxes(a, issued, landed);
+}
 
 // columns n0 .. n0 + 31 of row m
 __device__ __forceinline__ void store_row32(const F8Args& a, int64_t m, int64_t n0, const float2 (&acc)[16])
@@ -151,9 +184,7 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
                     tma_load_2d(sm.b[s], &tB, kb * GK, n0, &sm.full[s]);
                 }
             }
-            // no copy may be in flight when the block leaves: wait for the last boxes
-            for (int j = it > C::STAGES ? it - C::STAGES : 0; j < it; ++j)
-                mbar_wait_sleep(&sm.full[j % C::STAGES], (uint32_t)((j / C::STAGES) & 1));
+            await_boxes<C::STAGES>(a, sm.full, it);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -163,6 +194,10 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
         bool alive = true;
         for (int64_t tile = blockIdx.x; alive && tile < tiles; tile += gridDim.x) {
             for (int kb = 0; kb < KB; ++kb, ++it) {
+                if (test_withheld(a, it)) {
+                    alive = false;
+                    break;
+                }
                 const int s = it % C::STAGES, slot = it % C::ACC;
                 const bool got = (it < C::ACC || mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / C::ACC - 1) & 1))) &&
                                  mbar_wait_sleep(&sm.full[s], (uint32_t)((it / C::STAGES) & 1));
@@ -320,10 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
                     tma_load_2d_pair(sm.b[s], &tB, kb * GK, n0, bar);
                 }
             }
-            // no copy of either CTA may be in flight when the pair leaves
-            if (rank == 0)
-                for (int j = it > PSTAGES ? it - PSTAGES : 0; j < it; ++j)
-                    mbar_wait_sleep(&sm.full[j % PSTAGES], (uint32_t)((j / PSTAGES) & 1));
+            if (rank == 0) await_boxes<PSTAGES>(a, sm.full, it);  // of both CTAs
         } else if (warp == 1 && rank == 0) {
             const uint64_t ad0 = sw128_desc(sm.a[0]), bd0 = sw128_desc(sm.b[0]);
             const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), leader = elect_lane();
@@ -331,6 +363,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
             bool alive = true;
             for (int64_t tile = tile0; alive && tile < tiles; tile += step) {
                 for (int kb = 0; kb < KB; ++kb, ++it) {
+                    if (test_withheld(a, it)) {
+                        alive = false;
+                        break;
+                    }
                     const int s = it % PSTAGES, slot = it % PACC;
                     const bool got = (it < PACC || mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / PACC - 1) & 1))) &&
                                      mbar_wait_sleep(&sm.full[s], (uint32_t)((it / PSTAGES) & 1));
@@ -547,28 +583,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            bool alive = true;
-            for (int kb = k0 + C::STAGES; alive && kb < k1; ++kb) {
-                const int it = kb - k0, s = it % C::STAGES;
+            int it = min(k1 - k0, C::STAGES);
+            for (; it < k1 - k0; ++it) {
+                const int s = it % C::STAGES, kb = k0 + it;
                 if (!mbar_wait_sleep(&sm.empty[s], (uint32_t)((it / C::STAGES - 1) & 1))) {
                     atomicOr(&sm.status, kStTimeout);
-                    alive = false;
                     break;
                 }
                 mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(GM * GK + NT * GK));
                 tma_load_2d(sm.w[s], &tW, kb * GK, n0, &sm.full[s]);
                 tma_load_2d(sm.a[s], &tA, kb * GK, 0, &sm.full[s]);
             }
-            // no copy may be in flight when the block leaves: wait for the last boxes
-            if (alive)
-                for (int it = k1 - k0 > C::STAGES ? k1 - k0 - C::STAGES : 0; it < k1 - k0; ++it)
-                    mbar_wait_sleep(&sm.full[it % C::STAGES], (uint32_t)((it / C::STAGES) & 1));
+            await_boxes<C::STAGES>(a, sm.full, it);
         }
         __syncwarp();
     } else if (warp == 1) {
         const uint64_t wd0 = sw128_desc(sm.w[0]), ad0 = sw128_desc(sm.a[0]);
         const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), leader = elect_lane();
         for (int it = 0; it < k1 - k0; ++it) {
+            if (test_withheld(a, it)) break;
             const int s = it % C::STAGES, slot = it % C::ACC;
             const bool got = (it < C::ACC || mbar_wait_sleep(&sm.acc_empty[slot], (uint32_t)((it / C::ACC - 1) & 1))) &&
                              mbar_wait_sleep(&sm.full[s], (uint32_t)((it / C::STAGES) & 1));
@@ -703,14 +736,9 @@ cudaError_t launch_gemm_fp8(const F8Args& a, const CUtensorMap& ta, const CUtens
     return cudaGetLastError();
 }
 
-}  // namespace
-}  // namespace hq
-
-using namespace hq;
-
-extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W, int64_t ldw,
-                                   const float* sw, int64_t N, int64_t K, void* Y, hq_dtype_t ydtype, void* ws,
-                                   size_t ws_bytes, void* stream)
+hq_status_t gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W, int64_t ldw, const float* sw,
+                     int64_t N, int64_t K, void* Y, hq_dtype_t ydtype, void* ws, size_t ws_bytes, void* stream, int test_silent,
+                     uint32_t* test_log)
 {
     if (!A || !sa || !W || !sw || !Y || M < 1 || N < 1 || K < 1 || lda < K || ldw < K || lda % 16 || ldw % 16) return HQ_ERR_ARG;
     if (ydtype != HQ_BF16 && ydtype != HQ_F32) return HQ_ERR_ARG;
@@ -723,7 +751,7 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
     if (!dev.ok) return HQ_ERR_ARG;
     const int64_t sms = num_sms(), mt = (M + GM - 1) / GM, kbs = (K + GK - 1) / GK, slabs = (N + GM - 1) / GM;
     F8Args a{M, N, K, sa, sw, Y, ydtype == HQ_BF16, ((y | (uintptr_t)N * es) & 15u) == 0, GM,
-             static_cast<WsHeader*>(ws)};
+             static_cast<WsHeader*>(ws), test_silent, test_log};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     CUtensorMap ta, tb;
     // A block of the tiled kernel takes about 0.25 us (a TMA round trip is hidden by the ring, the issue of its
@@ -755,3 +783,26 @@ extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* s
                                     : (gn == 64 ? launch_gemm_fp8<64>(a, ta, tb, st) : launch_gemm_fp8<32>(a, ta, tb, st));
     return e == cudaSuccess ? HQ_OK : HQ_ERR_CUDA;
 }
+
+}  // namespace
+}  // namespace hq
+
+using namespace hq;
+
+extern "C" hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W, int64_t ldw,
+                                   const float* sw, int64_t N, int64_t K, void* Y, hq_dtype_t ydtype, void* ws,
+                                   size_t ws_bytes, void* stream)
+{
+    return gemm_fp8(A, lda, sa, M, W, ldw, sw, N, K, Y, ydtype, ws, ws_bytes, stream, -1, nullptr);
+}
+
+#ifdef HQ_TEST_HOOKS
+// only in the test library (libhq_test.so): the product library does not export it
+extern "C" hq_status_t hq_test_gemm_fp8_silent_block(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W,
+                                                     int64_t ldw, const float* sw, int64_t N, int64_t K, void* Y, hq_dtype_t ydtype,
+                                                     void* ws, size_t ws_bytes, int32_t silent_block, uint32_t* log, void* stream)
+{
+    if (silent_block < 0 || !log) return HQ_ERR_ARG;
+    return gemm_fp8(A, lda, sa, M, W, ldw, sw, N, K, Y, ydtype, ws, ws_bytes, stream, silent_block, log);
+}
+#endif

@@ -329,10 +329,10 @@ __global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
         for (int i = 0; i < count; ++i) {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sm.full[warp][stage], parity))) {
                 status |= kStTimeout;
-                for (int j = i + 1; j < count && j < i + STAGES; ++j) {  // the copies of the other stages land first
+                for (int j = i; j < count && j < i + STAGES; ++j) {  // the copies under way land first, if they ever do
+                    mbar_wait(&sm.full[warp][stage], parity);
                     stage = stage + 1 == STAGES ? 0 : stage + 1;
                     parity ^= stage == 0;
-                    mbar_wait(&sm.full[warp][stage], parity);
                 }
                 dead = true;
                 break;
