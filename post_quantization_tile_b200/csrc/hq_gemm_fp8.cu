@@ -51,6 +51,7 @@ struct F8Smem {
     uint64_t empty[C::STAGES];
     uint64_t acc_full[C::ACC];
     uint64_t acc_empty[C::ACC];
+    uint64_t drain;  // the MMAs
     uint32_t tmem_base;
     uint32_t status;
 };
@@ -64,7 +65,7 @@ struct F8Args {
     int box_m;  // rows of A's boxes: fewer than the tile's 128 where A has fewer (the rest of the stage is never stored)
     WsHeader* ws;
     // read only by the test build (HQ_TEST_HOOKS): the block of every CTA whose MMAs are withheld, so that the
-    // waits behind it run out, and two words a CTA, boxes asked for and boxes awaited at the end
+    // waits behind it run out, and three words a CTA: boxes asked for, boxes awaited, MMAs awaited at the end
     int test_silent;
     uint32_t* test_log;
 };
@@ -80,8 +81,14 @@ __device__ __forceinline__ bool test_withheld(const F8Args& a, int it)
 __device__ __forceinline__ void test_boxes(const F8Args& a, int issued, int awaited)
 {
 #ifdef HQ_TEST_HOOKS
-    a.test_log[2 * blockIdx.x] = issued;
-    a.test_log[2 * blockIdx.x + 1] = awaited;
+    a.test_log[3 * blockIdx.x] = issued;
+    a.test_log[3 * blockIdx.x + 1] = awaited;
+#endif
+}
+__device__ __forceinline__ void test_drained(const F8Args& a, bool done)
+{
+#ifdef HQ_TEST_HOOKS
+    a.test_log[3 * blockIdx.x + 2] = done;
 #endif
 }
 
@@ -157,6 +164,7 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
             mbar_init(&sm.acc_full[s], 1);
             mbar_init(&sm.acc_empty[s], C::EPI);
         }
+        mbar_init(&sm.drain, 1);
         sm.status = 0u;
         fence_mbar_init();
     }
@@ -215,6 +223,10 @@ __global__ void __launch_bounds__(F8Cfg<GN>::THREADS, 1)
                 mma_commit_warp(&sm.acc_full[slot], leader);
             }
         }
+        // after a timeout the epilogue may not have waited for the last MMAs: none may be under way when the
+        // tensor memory is given back
+        mma_commit_warp(&sm.drain, leader);
+        test_drained(a, mbar_wait_sleep(&sm.drain, 0));
     } else {
         // warpgroup h takes columns 32 h .. 32 h + 31 of each slot; a warp reads the TMEM lane quarter
         // warp % 4, one row of the tile per thread
@@ -285,6 +297,7 @@ struct PairSmem {
     uint64_t empty[PSTAGES];
     uint64_t acc_full[PACC];
     uint64_t acc_empty[PACC];
+    uint64_t drain;  // the MMAs
     uint32_t tmem_base;
     uint32_t status;
 };
@@ -324,6 +337,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
             mbar_init(&sm.acc_full[s], 1);
             mbar_init(&sm.acc_empty[s], 2 * PEPI);  // even CTA: both CTAs' epilogue warps
         }
+        mbar_init(&sm.drain, 1);
         sm.status = 0u;
         fence_mbar_init();
     }
@@ -384,6 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
                     mma_commit_pair(&sm.acc_full[slot], leader);
                 }
             }
+            mma_commit_pair(&sm.drain, leader, 1);  // as in the kernel above
+            test_drained(a, mbar_wait_sleep(&sm.drain, 0));
         }
         __syncwarp();
     } else {
@@ -534,6 +550,7 @@ struct FewSmem {
     uint64_t empty[C::STAGES];
     uint64_t acc_full[C::ACC];
     uint64_t acc_empty[C::ACC];
+    uint64_t drain;  // the MMAs
     uint32_t tmem_base;
     uint32_t status;
 };
@@ -565,6 +582,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             mbar_init(&sm.acc_full[s], 1);
             mbar_init(&sm.acc_empty[s], 4);
         }
+        mbar_init(&sm.drain, 1);
         sm.status = 0u;
         fence_mbar_init();
         // the first loads need none of the other warps
@@ -617,6 +635,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             mma_commit_warp(&sm.empty[s], leader);
             mma_commit_warp(&sm.acc_full[slot], leader);
         }
+        mma_commit_warp(&sm.drain, leader);  // as in the kernels above
+        test_drained(a, mbar_wait_sleep(&sm.drain, 0));
     }
     float2 acc[NT / 2];
     const int q = warp & 3, row = q * 32 + lane;

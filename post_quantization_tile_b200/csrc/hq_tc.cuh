@@ -164,12 +164,13 @@ __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uin
         ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
-// arrive on `bar` of both CTAs once every MMA issued so far by the warp's elected lane has completed
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t leader)
+// arrive on `bar` of both CTAs (or those of the bits of `ctas`) once every MMA issued so far by the warp's
+// elected lane has completed
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t leader, uint16_t ctas = 3)
 {
     asm volatile("{\n\t.reg .pred one;\n\tsetp.ne.b32 one, %2, 0;\n\t"
                  "@one tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n"
-                 ::"r"(smem_u32(bar)), "h"((uint16_t)3), "r"(leader)
+                 ::"r"(smem_u32(bar)), "h"(ctas), "r"(leader)
                  : "memory");
 }
 

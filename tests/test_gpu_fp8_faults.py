@@ -35,7 +35,7 @@ def run(hq, silent, M, N, K_, block):
     a = hq.fp8_quantize(torch.randn(M, K_, generator=g).cuda())
     w = hq.fp8_quantize(torch.randn(N, K_, generator=g).cuda(), block=128)
     ref = hq.gemm_fp8(a, w)
-    y, ws, log = torch.empty_like(ref), hq.fp8_workspace(), torch.zeros(4096, 2, dtype=torch.int32, device="cuda")
+    y, ws, log = torch.empty_like(ref), hq.fp8_workspace(), torch.zeros(4096, 3, dtype=torch.int32, device="cuda")
     ld = a.data.shape[1]
     assert silent(a.data.data_ptr(), ld, a.scale.data_ptr(), M, w.data.data_ptr(), ld, w.scale.data_ptr(), N, K_, y.data_ptr(), 0,
                   ws.ptr(), ws.nbytes, block, log.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
@@ -49,5 +49,11 @@ def run(hq, silent, M, N, K_, block):
 def test_no_box_is_under_way_after_a_timeout(hq, silent, M, N, K_, block, stages):
     log = run(hq, silent, M, N, K_, block)
     assert len(log)
-    for issued, landed in log.tolist():
+    for issued, landed, _ in log.tolist():
         assert issued == block + stages and landed == stages
+
+
+@pytest.mark.parametrize("M,N,K_,block,stages", CASES)
+def test_no_tensor_core_work_is_under_way_after_a_timeout(hq, silent, M, N, K_, block, stages):
+    log = run(hq, silent, M, N, K_, block)
+    assert len(log) and torch.all(log[:, 2] == 1)
