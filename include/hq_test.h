@@ -36,7 +36,8 @@ hq_status_t hq_test_encode_silent_item(const void* x, hq_dtype_t dtype, int64_t 
  * second each).  Expect HQ_ERR_TIMEOUT from hq_status_read where a thread block has that many, and a product
  * that is not usable.  log (device, zeroed by the caller, 3 * 4096 words): for each thread block that waits for
  * operands, how many boxes it asked for, how many of the last of them, as many as its ring has stages,
- * it saw land before it left, and whether it saw its tensor-core work end.
+ * it saw land before it left, and whether it saw its tensor-core work end.  Of a pair of thread blocks the
+ * even one waits for both; here it asks for two boxes less than the odd one, as if its wait had run out first.
  */
 hq_status_t hq_test_gemm_fp8_silent_block(const uint8_t* A, int64_t lda, const float* sa, int64_t M, const uint8_t* W,
                                           int64_t ldw, const float* sw, int64_t N, int64_t K, void* Y, hq_dtype_t ydtype,

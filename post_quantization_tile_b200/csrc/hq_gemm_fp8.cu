@@ -298,6 +298,8 @@ struct PairSmem {
     uint64_t acc_full[PACC];
     uint64_t acc_empty[PACC];
     uint64_t drain;  // the MMAs
+    uint64_t peer_done;    // even CTA: the odd one has asked for its last box,
+    uint32_t peer_issued;  // of so many
     uint32_t tmem_base;
     uint32_t status;
 };
@@ -337,6 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
             mbar_init(&sm.acc_full[s], 1);
             mbar_init(&sm.acc_empty[s], 2 * PEPI);  // even CTA: both CTAs' epilogue warps
         }
+        mbar_init(&sm.peer_done, 1);
         mbar_init(&sm.drain, 1);
         sm.status = 0u;
         fence_mbar_init();
@@ -358,6 +361,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
                 const int m0 = at.m * 2 * GM + (int)rank * GM, n0 = at.n * PN + (int)rank * GM;
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % PSTAGES;
+                    if (rank == 0 && test_withheld(a, it - PSTAGES + 2)) {  // the test build: two boxes less than the odd CTA
+                        alive = false;
+                        break;
+                    }
                     if (it >= PSTAGES && !mbar_wait_sleep(&sm.empty[s], (uint32_t)((it / PSTAGES - 1) & 1))) {
                         atomicOr(&sm.status, kStTimeout);
                         alive = false;
@@ -369,7 +376,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
                     tma_load_2d_pair(sm.b[s], &tB, kb * GK, n0, bar);
                 }
             }
-            if (rank == 0) await_boxes<PSTAGES>(a, sm.full, it);  // of both CTAs
+            // The odd CTA's boxes complete on the even one's barriers.  Where one of them ran out of time, the
+            // other may have asked for more boxes: the even CTA waits for the boxes of both.
+            if (rank == 1) {
+                st_cluster(peer_addr(&sm.peer_issued, 0), (uint32_t)it);
+                mbar_arrive_release(peer_addr(&sm.peer_done, 0));
+            } else {
+                const int peer = mbar_wait_acquire(&sm.peer_done, 0) ? (int)sm.peer_issued : it;
+                for (int j = it; j < peer; ++j) mbar_arrive_expect_tx(&sm.full[j % PSTAGES], 2u * GM * GK);
+                await_boxes<PSTAGES>(a, sm.full, max(it, peer));
+            }
         } else if (warp == 1 && rank == 0) {
             const uint64_t ad0 = sw128_desc(sm.a[0]), bd0 = sw128_desc(sm.b[0]);
             const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tbase, 0), leader = elect_lane();
@@ -555,11 +571,6 @@ struct FewSmem {
     uint32_t status;
 };
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float x)
-{
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
-}
-
 template <int NT>
 __global__ void __launch_bounds__(kFewThreads, 1)
     gemm_fp8_few_kernel(const F8Args a, const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tW, int parts)
@@ -701,7 +712,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const float x = c & 1 ? acc[c / 2].y : acc[c / 2].x;
             const int owner = c / share;
             float* to = &sm.red[(rank * share + c - owner * share) * GM + row];
-            if (parts > 1) st_cluster(peer_addr(to, (uint32_t)owner), x);
+            if (parts > 1) st_cluster(peer_addr(to, (uint32_t)owner), __float_as_uint(x));
             else *to = x;
         }
     }
