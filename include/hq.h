@@ -455,7 +455,8 @@ hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t ws_bytes, v
  *             of the probabilities it received from its head's rows, added to weights_in (same shape;
  *             NULL: 0; may be weights itself).  Slots behind are left as they were; slots j >= L are
  *             dropped (HQ_ERR_RANGE).
- *   ws        hq_kv8_attend_workspace_bytes(B, heads, Hq, Sq, dim, weights != NULL) bytes, 256-byte aligned
+ *   ws        hq_kv8_attend_workspace_need(p) bytes, 256-byte aligned; hq_kv8_attend_workspace_bytes(B, heads, Hq,
+ *             Sq, dim, weights != NULL) is what the longest table takes
  * Products take bf16 queries (elements down to 2^-31 of a row's largest) and codes exactly, whatever the
  * pages' scales, and accumulate in binary32; probabilities enter the second product as binary16.  B <= 2048.  The result does not depend on the other sequences' content.
  */
@@ -479,6 +480,7 @@ typedef struct {
     int64_t L;
 } hq_kv8_attend_t;
 size_t hq_kv8_attend_workspace_bytes(int64_t B, int32_t heads, int64_t Hq, int64_t Sq, int32_t dim, int32_t weights);
+size_t hq_kv8_attend_workspace_need(const hq_kv8_attend_t* p);
 hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t ws_bytes, void* stream);
 
 /*

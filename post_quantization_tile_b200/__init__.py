@@ -122,6 +122,8 @@ def lib():
             getattr(L, f).argtypes = [ctypes.c_char_p, P, ctypes.c_size_t, P]
         L.hq_kv8_attend_workspace_bytes.argtypes = [i64, i32, i64, i64, i32, i32]
         L.hq_kv8_attend_workspace_bytes.restype = ctypes.c_size_t
+        L.hq_kv8_attend_workspace_need.argtypes = [ctypes.c_char_p]
+        L.hq_kv8_attend_workspace_need.restype = ctypes.c_size_t
         L.hq_kv8_evict_workspace_bytes.argtypes = [i64, i32, i64]
         L.hq_kv8_evict_workspace_bytes.restype = ctypes.c_size_t
         L.hq_status_read.argtypes = [P, P, ctypes.POINTER(ctypes.c_int64)]

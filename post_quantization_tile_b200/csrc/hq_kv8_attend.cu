@@ -29,6 +29,8 @@
 //     units of the last value scale and multiplied by the (power-of-two) ratio when that changes.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "hq_kv8_attend.cuh"
 
 namespace hq {
@@ -522,14 +524,21 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 // slots, dim 128, four sequences: 32 rows 29.0 us here against 32.9 there, 64 rows 39.9 against 34.2; sixteen
 // sequences: 63.8 against 80.9 and 111.5 against 85.4.
 bool many_rows(int64_t rows) { return rows > 32; }
-constexpr int kMaxGridFew = 512, kMaxGridMany = 256;
+constexpr int kMaxGridFew = 3 * 148, kMaxGridMany = 148;  // thread blocks: residents of an SM times SMs, at most
 
 struct AttendLayout {
     size_t prefix, len, part_o, part_ml, lse2, bytes;
 };
-AttendLayout attend_layout(int64_t B, int64_t Hq, int64_t Sq, int64_t D, bool weights, bool many)
+// slots: of a sequence's table.  Parts: two of a unit's rows for each share, and a share has two tiles at least
+// (share_count).
+AttendLayout attend_layout(int64_t B, int64_t heads, int64_t Hq, int64_t Sq, int64_t D, int64_t slots, bool weights)
 {
-    const size_t parts = many ? (size_t)2 * kMaxGridMany * kManyRows : (size_t)2 * kMaxGridFew * 16;
+    const int64_t rows = Sq * (Hq / heads);
+    const bool many = many_rows(rows);
+    const int64_t unit = many ? kManyRows : (rows <= 8 ? 8 : 16), grid = many ? kMaxGridMany : kMaxGridFew;
+    const int64_t tile = many ? 128 : 64, units = B * heads * ((rows + unit - 1) / unit), tiles = (slots + tile - 1) / tile;
+    const int64_t shares = tiles > 2 * grid || units > 2 * grid ? grid : std::min(grid, (units * tiles + 1) / 2);
+    const size_t parts = (size_t)(2 * shares * unit);
     AttendLayout l;
     l.prefix = align256(kSlotBytes);
     l.len = l.prefix + align256(sizeof(uint32_t) * (size_t)(B + 2));
@@ -581,7 +590,15 @@ extern "C" size_t hq_kv8_attend_workspace_bytes(int64_t B, int32_t heads, int64_
     if (B < 1 || B > kMaxBatch || heads < 1 || Hq < heads || Hq % heads || Sq < 1 || (D != 64 && D != 128) || Hq > 65535 ||
         Sq > ((int64_t)1 << 24))
         return 0;
-    return attend_layout(B, Hq, Sq, D, weights != 0, many_rows(Sq * (Hq / heads))).bytes;
+    return attend_layout(B, heads, Hq, Sq, D, (int64_t)1 << 30, weights != 0).bytes;
+}
+
+extern "C" size_t hq_kv8_attend_workspace_need(const hq_kv8_attend_t* p)
+{
+    if (!p || p->max_pages < 1 || p->max_pages > ((int64_t)1 << 24) || !kv8_shape_supported(&p->cache) ||
+        !hq_kv8_attend_workspace_bytes(p->B, p->cache.heads, p->Hq, p->Sq, p->cache.dim, 0))
+        return 0;
+    return attend_layout(p->B, p->cache.heads, p->Hq, p->Sq, p->cache.dim, p->max_pages * p->cache.page, p->weights != nullptr).bytes;
 }
 
 extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t ws_bytes, void* stream)
@@ -610,7 +627,7 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     if ((p->weights_in && !p->weights) || p->out == p->q) return HQ_ERR_ARG;
     if (p->weights && p->B > 65535) return HQ_ERR_UNSUPPORTED;
     const bool many = many_rows(p->Sq * G);
-    const AttendLayout l = attend_layout(p->B, p->Hq, p->Sq, p->cache.dim, p->weights != nullptr, many);
+    const AttendLayout l = attend_layout(p->B, H, p->Hq, p->Sq, p->cache.dim, slots, p->weights != nullptr);
     if (ws_bytes < l.bytes) return HQ_ERR_ARG;
     DeviceGuard dev(p->cache.k);
     if (!dev.ok) return HQ_ERR_ARG;

@@ -337,7 +337,7 @@ PyObject* kv8_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
         } else if (a[13] != Py_None) {
             refuse("weights_in without weights");
         }
-        const size_t need = a[14] != Py_None ? 0 : hq_kv8_attend_workspace_bytes(p.B, c.c.heads, p.Hq, p.Sq, c.c.dim, p.weights != nullptr);
+        const size_t need = a[14] != Py_None ? 0 : hq_kv8_attend_workspace_need(&p);
         const Scratch w = scratch(a[14], c.dev, need);
         if (failed(hq_kv8_attend(&p, w.ptr, w.bytes, stream_of(c.dev)), "hq_kv8_attend")) return nullptr;
         return THPVariable_Wrap(std::move(out));
