@@ -447,7 +447,7 @@ hq_status_t hq_kv8_append(const hq_kv8_append_t* p, void* ws, size_t ws_bytes, v
  * of 8, 16-byte aligned bases), query head i reads key head i / (Hq / heads).
  *   lens      [B] slots of each sequence (the queries' own tokens among them)
  *   q_lens    [B] queries of each sequence, NULL: Sq; rows behind them are left as they were.  out may
- *             not overlap q
+ *             not overlap q, and no row of an output another one (a stride of 0 is refused)
  *   causal    0: a query sees all lens[b] slots; 1: query i of m sees slots 0 .. lens[b] - m + i
  *   lse       [B, Hq, Sq] fp32 (strides of b and head) natural logarithm of the sum of exp(scale q.k),
  *             or NULL.  A row that sees nothing gives zeros and -infinity.
@@ -490,8 +490,8 @@ hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t ws_bytes, v
  * keeps its own slots.  They are moved, in order, to slots 0 .. of the pages to_table[b] (pages that no
  * sequence of the call reads, each of them once), a new page's scale being the largest of its tokens' old ones and
  * codes following as in hq_kv8_append; out_lens[b] = min(lens[b], budget) (may be lens itself).
- * weights [B, heads, L] and out_weights [B, heads, >= budget] (strides of b and head; NULL: not
- * wanted; another buffer than weights) hold the slots' weights before and after.
+ * weights [B, heads, L] and out_weights [B, heads, >= budget] (strides of b and head, not 0; NULL: not
+ * wanted; apart from weights) hold the slots' weights before and after.
  * ws: hq_kv8_evict_workspace_bytes(B, heads, budget) bytes.
  */
 typedef struct {

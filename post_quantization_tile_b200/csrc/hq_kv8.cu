@@ -539,6 +539,7 @@ extern "C" hq_status_t hq_kv8_evict(const hq_kv8_evict_t* p, void* ws, size_t ws
                          reinterpret_cast<uintptr_t>(p->weights) | reinterpret_cast<uintptr_t>(p->to_table) |
                          reinterpret_cast<uintptr_t>(p->out_lens) | reinterpret_cast<uintptr_t>(p->out_weights);
     if ((al & 3u) || (reinterpret_cast<uintptr_t>(ws) & 15u) || p->out_weights == p->weights) return HQ_ERR_ARG;
+    if (p->out_weights && expanded(p->ow_stride, {p->B, p->cache.heads})) return HQ_ERR_ARG;
     if (ws_bytes < hq_kv8_evict_workspace_bytes(p->B, p->cache.heads, p->budget)) return HQ_ERR_ARG;
     DeviceGuard dev(p->cache.k);
     if (!dev.ok) return HQ_ERR_ARG;

@@ -21,6 +21,15 @@ inline bool kv8_shape_supported(const hq_kv8_t* c)
     return (c->dim == 64 || c->dim == 128) && (c->page == 16 || c->page == 32 || c->page == 64 || c->page == 128);
 }
 
+// whether rows of an output share memory: a dimension longer than one without a stride
+template <int N>
+inline bool expanded(const int64_t (&stride)[N], const int64_t (&length)[N])
+{
+    for (int i = 0; i < N; ++i)
+        if (stride[i] == 0 && length[i] > 1) return true;
+    return false;
+}
+
 inline int page_shift_of(int page) { return page == 16 ? 4 : (page == 32 ? 5 : (page == 64 ? 6 : 7)); }
 
 }  // namespace hq

@@ -625,6 +625,9 @@ extern "C" hq_status_t hq_kv8_attend(const hq_kv8_attend_t* p, void* ws, size_t 
     if ((al & 3u) || (reinterpret_cast<uintptr_t>(ws) & 255u)) return HQ_ERR_ARG;
     if (p->weights && p->L < 1) return HQ_ERR_ARG;
     if ((p->weights_in && !p->weights) || p->out == p->q) return HQ_ERR_ARG;
+    if (expanded(p->out_stride, {p->B, p->Hq, p->Sq}) || (p->lse && expanded(p->lse_stride, {p->B, p->Hq})) ||
+        (p->weights && expanded(p->w_stride, {p->B, H})))
+        return HQ_ERR_ARG;
     if (p->weights && p->B > 65535) return HQ_ERR_UNSUPPORTED;
     const bool many = many_rows(p->Sq * G);
     const AttendLayout l = attend_layout(p->B, H, p->Hq, p->Sq, p->cache.dim, slots, p->weights != nullptr);

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -15,6 +16,7 @@
 
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "../../include/hq.h"
 
@@ -116,6 +118,49 @@ int64_t whole(PyObject* o, const char* name)
 void strides(const at::Tensor& t, int64_t* to, int n)
 {
     for (int i = 0; i < n; ++i) to[i] = t.size(i) == 1 ? 0 : t.stride(i);
+}
+
+// an output whose rows are distinct: an expanded one would be written by several rows at once
+const at::Tensor& output(const at::Tensor& t, const char* name)
+{
+    if (at::has_internal_overlap(t) == at::MemOverlap::Yes) refuse(std::string(name) + " is expanded: its rows share memory");
+    return t;
+}
+
+// whether rows of la elements from 0 and of lb elements from d, both repeated n[k] times at strides s[k] (the
+// largest first, each spanning the ones behind it), have an element in common
+bool rows_meet(int64_t d, const int64_t* s, const int64_t* n, int dims, int64_t la, int64_t lb)
+{
+    if (dims == 0) return d < la && d > -lb;
+    if (n[0] == 1 || s[0] < 1) return rows_meet(d, s + 1, n + 1, dims - 1, la, lb);
+    const int64_t i = d / s[0];
+    for (int64_t j = i - 1; j <= i + 1; ++j)
+        if (j > -n[0] && j < n[0] && rows_meet(d - j * s[0], s + 1, n + 1, dims - 1, la, lb)) return true;
+    return false;
+}
+// an output may not share memory with an input that other rows still read; the very same view is left to the caller
+void apart(const at::Tensor& out, const at::Tensor& in, const char* names)
+{
+    if (!out.is_alias_of(in)) return;
+    const int dims = (int)out.dim() - 1;
+    const int64_t d = in.storage_offset() - out.storage_offset();
+    bool same = true;
+    int64_t s[3], n[3];
+    for (int i = 0; i < dims; ++i) {
+        s[i] = out.size(i) == 1 ? 0 : out.stride(i);
+        n[i] = out.size(i);
+        same = same && out.size(i) == in.size(i) && (n[i] == 1 || s[i] == in.stride(i));
+    }
+    if (same && d == 0 && out.sizes() == in.sizes()) return;
+    bool meet;
+    if (same) {
+        for (int i = 1; i < dims; ++i)
+            for (int j = i; j > 0 && s[j] > s[j - 1]; --j) std::swap(s[j], s[j - 1]), std::swap(n[j], n[j - 1]);
+        meet = rows_meet(d, s, n, dims, out.size(dims), in.size(dims));
+    } else {
+        meet = at::get_overlap_status(out, in) == at::MemOverlapStatus::Partial;
+    }
+    if (meet) refuse(std::string(names) + " overlap");
 }
 
 struct Cache {
@@ -295,7 +340,8 @@ PyObject* kv8_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
         p.cache = c.c;
         p.q = on(a[4], "q", c.dev, at::kBFloat16, shape, kRows).data_ptr();
         at::Tensor out = a[10] == Py_None ? make(c.dev, at::kBFloat16, shape) : on(a[10], "out", c.dev, at::kBFloat16, shape, kRows);
-        p.out = out.data_ptr();
+        p.out = output(out, "out").data_ptr();
+        apart(out, q, "out and q");
         p.B = shape[0];
         p.Hq = shape[1];
         p.Sq = shape[2];
@@ -317,7 +363,7 @@ PyObject* kv8_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
         for (int i = 0; i < 2; ++i) p.win_stride[i] = p.w_stride[i] = 0;
         p.L = 0;
         if (a[11] != Py_None) {
-            const at::Tensor& x = on(a[11], "lse", c.dev, at::kFloat, shape.slice(0, 3), kRows);
+            const at::Tensor& x = output(on(a[11], "lse", c.dev, at::kFloat, shape.slice(0, 3), kRows), "lse");
             p.lse = (float*)x.data_ptr();
             p.lse_stride[0] = x.stride(0);
             p.lse_stride[1] = x.stride(1);
@@ -325,11 +371,12 @@ PyObject* kv8_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (a[12] != Py_None) {
             const at::Tensor& x = tensor(a[12], "weights");
             p.L = x.dim() == 3 ? x.size(2) : 0;
-            p.weights = (float*)on(a[12], "weights", c.dev, at::kFloat, {p.B, c.c.heads, p.L}, kRows).data_ptr();
+            p.weights = (float*)output(on(a[12], "weights", c.dev, at::kFloat, {p.B, c.c.heads, p.L}, kRows), "weights").data_ptr();
             p.w_stride[0] = x.stride(0);
             p.w_stride[1] = x.stride(1);
             if (a[13] != Py_None) {
                 const at::Tensor& y = on(a[13], "weights_in", c.dev, at::kFloat, {p.B, c.c.heads, p.L}, kRows);
+                apart(x, y, "weights and weights_in");
                 p.weights_in = (const float*)y.data_ptr();
                 p.win_stride[0] = y.stride(0);
                 p.win_stride[1] = y.stride(1);
@@ -372,13 +419,15 @@ PyObject* kv8_evict(PyObject*, PyObject* const* a, Py_ssize_t n)
         p.recent = whole(a[8], "recent");
         if (p.budget < 1 || p.recent < 0) refuse("budget must be at least 1 and recent at least 0");
         at::Tensor lens = a[10] == Py_None ? make(c.dev, at::kInt, {p.B}) : on(a[10], "out_lens", c.dev, at::kInt, {p.B}, kWhole);
+        apart(lens, tensor(a[5], "lens"), "out_lens and lens");
         at::Tensor ow;
         if (a[11] == Py_None) {
             ow = at::zeros({p.B, c.c.heads, p.budget}, x.options());
         } else {
             ow = tensor(a[11], "out_weights");
             if (ow.dim() != 3 || ow.size(2) < p.budget) refuse("out_weights needs room for the budget");
-            on(a[11], "out_weights", c.dev, at::kFloat, {p.B, c.c.heads, ow.size(2)}, kRows);
+            output(on(a[11], "out_weights", c.dev, at::kFloat, {p.B, c.c.heads, ow.size(2)}, kRows), "out_weights");
+            apart(ow, x, "out_weights and weights");
         }
         p.out_lens = (int32_t*)lens.data_ptr();
         p.out_weights = (float*)ow.data_ptr();

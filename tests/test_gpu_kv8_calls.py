@@ -59,3 +59,98 @@ def test_a_short_call_of_many_rows_takes_little_scratch(hq):
     before = torch.cuda.memory_allocated()
     hq.kv8_attend(q, cache, t, n, out=out)
     assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+def views(n, rows, dim, dtype):
+    """(output, input) pairs of views of one buffer: rows that meet, and rows that do not."""
+    def buf(*shape):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+    a, b, c = buf(2 * n * rows * dim + 64), buf(n, rows, 2, dim), buf(n, 2 * rows, dim)
+    whole = a[:n * rows * dim].view(n, rows, dim)
+    meet = [(a[8:8 + n * rows * dim].view(n, rows, dim), whole), (whole, a[dim:dim + n * rows * dim].view(n, rows, dim)),
+            (whole, a[(n * rows - 1) * dim:(2 * n * rows - 1) * dim].view(n, rows, dim)), (c[:, :rows], c[:, rows - 1:-1])]
+    apart = [(b[:, :, 0], b[:, :, 1]), (b[:, :, 1], b[:, :, 0]), (c[:, :rows], c[:, rows:]), (c[:, rows:], c[:, :rows]),
+             (whole, a[n * rows * dim:2 * n * rows * dim].view(n, rows, dim))]
+    return meet, apart
+
+
+def test_attend_refuses_outputs_that_meet_their_inputs(hq):
+    """out and q, weights and weights_in of one buffer: refused where rows meet, computed where they do not."""
+    cache, _, table = setup_cache(hq, gen(4), 3, 2, 4, 16, 64)
+    t, n = i32(table), i32([20, 3, 32])
+    x = torch.randn(3, 4, 64, generator=gen(5)).to(torch.bfloat16).cuda()
+    ref = hq.kv8_attend(x.view(3, 4, 1, 64), cache, t, n)
+    meet, apart = views(3, 4, 64, torch.bfloat16)
+    for out, q in meet:
+        with pytest.raises(ValueError):
+            hq.kv8_attend(q.unsqueeze(2), cache, t, n, out=out.unsqueeze(2))
+    for out, q in apart:
+        q.copy_(x)
+        assert torch.equal(hq.kv8_attend(q.unsqueeze(2), cache, t, n, out=out.unsqueeze(2)), ref)
+    q, win = x.view(3, 4, 1, 64), torch.rand(3, 4, 32, generator=gen(6)).cuda()
+    want = win.clone()
+    hq.kv8_attend(q, cache, t, n, weights=want, weights_in=want)
+    meet, apart = views(3, 4, 32, torch.float32)
+    for w, w_in in meet:
+        with pytest.raises(ValueError):
+            hq.kv8_attend(q, cache, t, n, weights=w, weights_in=w_in)
+    for w, w_in in apart:
+        w_in.copy_(win)
+        w.copy_(win)
+        hq.kv8_attend(q, cache, t, n, weights=w, weights_in=w_in)
+        assert torch.equal(w, want)
+
+
+def test_evict_refuses_outputs_that_meet_their_inputs(hq):
+    cache, _, both = setup_cache(hq, gen(7), 3, 4, 4, 16, 64)
+    table, to, lens = i32(both[:, :2]), i32(both[:, 2:]), i32([32, 9, 20])
+    x = torch.rand(3, 4, 32, generator=gen(8)).cuda()
+    _, ref = hq.kv8_evict(cache, table, lens, x, 32, 4, to)
+    meet, apart = views(3, 4, 32, torch.float32)
+    for ow, w in meet + [(x[:, :, 3:], x)]:
+        with pytest.raises(ValueError):
+            hq.kv8_evict(cache, table, lens, w, 29 if ow.shape[2] == 29 else 32, 4, to, out_weights=ow)
+    for ow, w in apart:
+        w.copy_(x)
+        ow.zero_()
+        assert torch.equal(hq.kv8_evict(cache, table, lens, w, 32, 4, to, out_weights=ow)[1], ref)
+    ints = torch.zeros(8, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        hq.kv8_evict(cache, table, ints[:3], x, 8, 4, to, out_lens=ints[1:4])
+
+
+def test_expanded_outputs_are_refused(hq):
+    cache, _, table = setup_cache(hq, gen(9), 2, 2, 2, 16, 64)
+    t, n, q = i32(table), i32([20, 3]), torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device="cuda")
+    for shape in ((1, 4, 3, 64), (2, 1, 3, 64), (2, 4, 1, 64)):
+        with pytest.raises(ValueError):
+            hq.kv8_attend(q, cache, t, n, out=torch.zeros(shape, dtype=torch.bfloat16, device="cuda").expand(2, 4, 3, 64))
+    w = torch.zeros(1, 2, 32, device="cuda").expand(2, 2, 32)
+    with pytest.raises(ValueError):
+        hq.kv8_attend(q, cache, t, n, lse=torch.zeros(2, 1, 3, device="cuda").expand(2, 4, 3))
+    with pytest.raises(ValueError):
+        hq.kv8_attend(q, cache, t, n, weights=w)
+    with pytest.raises(ValueError):
+        hq.kv8_evict(cache, t, n, w.contiguous(), 16, 2, t, out_weights=torch.zeros(2, 1, 16, device="cuda").expand(2, 2, 16))
+    # inputs may be: every row of q and of the weights is the same
+    one = torch.randn(1, 1, 1, 64, generator=gen(10)).to(torch.bfloat16).cuda()
+    assert torch.equal(hq.kv8_attend(one.expand(2, 4, 3, 64), cache, t, n), hq.kv8_attend(one.expand(2, 4, 3, 64).contiguous(), cache, t, n))
+
+
+def test_expanded_outputs_are_refused_at_the_c_entry_points(hq):
+    from test_fp8_arguments import EVICT
+    cache, _, table = setup_cache(hq, gen(9), 2, 2, 2, 16, 64)
+    t, n, q = i32(table), i32([20, 3]), torch.zeros(2, 4, 3, 64, dtype=torch.bfloat16, device="cuda")
+    lib, ws, stream = hq.lib(), hq.Workspace(1 << 26), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    out = torch.zeros_like(q)
+    assert lib.hq_kv8_attend(attend_struct(hq, q, cache, t, n, out, None), ws.ptr(), ws.nbytes, stream) == 0
+    for i in range(3):
+        bad = out.narrow(i, 0, 1).expand_as(out)
+        assert lib.hq_kv8_attend(attend_struct(hq, q, cache, t, n, bad, None), ws.ptr(), ws.nbytes, stream) == 1
+    w = torch.zeros(2, 2, 32, device="cuda")
+    head = [x.data_ptr() for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)] + [cache.k.shape[0], 2, 16, 64]
+    to, ow = i32([[4], [5]]), torch.zeros(2, 2, 16, device="cuda")
+    for strides, code in (((32, 16), 0), ((0, 16), 1), ((32, 0), 1)):
+        args = EVICT.pack(*head, 2, t.data_ptr(), 2, 2, n.data_ptr(), w.data_ptr(), 64, 32, 32, 16, 2, to.data_ptr(), 1, 1, i32([0, 0]).data_ptr(),
+                          ow.data_ptr(), *strides)
+        assert lib.hq_kv8_evict(args, ws.ptr(), ws.nbytes, stream) == code
