@@ -356,7 +356,8 @@ PyObject* kv8_attend(PyObject*, PyObject* const* a, Py_ssize_t n)
         const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)c.c.dim) : PyFloat_AsDouble(a[8]);
         if (PyErr_Occurred()) return nullptr;
         p.scale = (float)scale;
-        p.causal = PyObject_IsTrue(a[9]) == 1;
+        p.causal = PyObject_IsTrue(a[9]);
+        if (p.causal < 0) return nullptr;
         p.lse = p.weights = nullptr;
         p.weights_in = nullptr;
         p.lse_stride[0] = p.lse_stride[1] = 0;

@@ -154,3 +154,17 @@ def test_expanded_outputs_are_refused_at_the_c_entry_points(hq):
         args = EVICT.pack(*head, 2, t.data_ptr(), 2, 2, n.data_ptr(), w.data_ptr(), 64, 32, 32, 16, 2, to.data_ptr(), 1, 1, i32([0, 0]).data_ptr(),
                           ow.data_ptr(), *strides)
         assert lib.hq_kv8_evict(args, ws.ptr(), ws.nbytes, stream) == code
+
+
+def test_causal_without_a_truth_value_raises_its_own_error(hq):
+    cache, _, table = setup_cache(hq, gen(11), 1, 2, 1, 16, 64)
+    q, t, n = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda"), i32(table), i32([20])
+
+    class Unsure:
+        def __bool__(self):
+            raise ZeroDivisionError
+    with pytest.raises(ZeroDivisionError):
+        hq.kv8_attend(q, cache, t, n, causal=Unsure())
+    with pytest.raises(TypeError):
+        hq.kv8_attend(q, cache, t, n, scale="wide")
+    assert hq.kv8_attend(q, cache, t, n, causal=0).shape == q.shape
