@@ -408,7 +408,9 @@ hq_status_t hq_gemm_fp8(const uint8_t* A, int64_t lda, const float* sa, int64_t 
  * of a page table (int32 page numbers) and a length (int32, device): slot j lies in page table[j / page]
  * at row j % page.  Page numbers outside the pool and lengths outside the table report HQ_ERR_RANGE;
  * slots of such pages are not read or written (attention treats them as unseen) and lengths are
- * clamped.  Bytes behind a sequence's length are never used: they may hold anything.
+ * clamped.  Bytes behind a sequence's length are never used: they may hold anything.  Slots before it hold
+ * no NaN codes (the append writes none): a NaN value would spoil rows that do not see its slot, as zero times
+ * NaN.
  */
 typedef struct {
     uint8_t* k;
@@ -423,7 +425,8 @@ typedef struct {
  * Append: tokens 0 .. n_new[b] - 1 of k, v [B, heads, S, dim] (element strides of b, head, token; dim
  * contiguous; base and strides multiples of 16 bytes) become slots lens[b] .. of sequence b.  A page's
  * scale becomes the larger of what its earlier tokens had and what the new ones need; where it grows,
- * the earlier codes q follow as the code nearest to q s_old / s_new.  A token's vector with NaN or
+ * the earlier codes q follow as the code nearest to q s_old / s_new.  (Scales that are no powers of two, which only
+ * a caller can have written: 1 / s, s_old / s_new and their products are rounded to binary32 first.)  A token's vector with NaN or
  * infinity is kept as zeros (HQ_ERR_NONFINITE, detail = vectors).  n_new NULL: S for every sequence.
  * Tokens past the table are dropped (HQ_ERR_RANGE).  lens is not changed.  A page that is appended to
  * belongs to one sequence only.  ws may be NULL (else hq_fp8_workspace_bytes()).

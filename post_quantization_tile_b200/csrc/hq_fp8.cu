@@ -9,8 +9,8 @@
 // two whole rows of the block.  Blocks of 1 x 128 reduce over their sixteen lanes, blocks of
 // 128 x 128 over the thread block that holds one of them.
 //
-// 11008 x 4096 bf16 in blocks of 128 x 128: 27.0 us, 5.0 TB/s, 76% of the copy rate (a block's wait between
-// its loads and its stores is the rest; streaming loads take 24.9 when replayed, but 30.7 against 28.8 in a
+// 11008 x 4096 bf16 in blocks of 128 x 128: 27.0 us, 5.0 TB/s, 76% of the copy rate (a block does not load
+// while it reduces and stores; streaming loads take 24.9 when replayed, but 30.7 against 28.8 in a
 // loop of calls); 8 x 4096 in blocks of 1 x 128: 1.7 us, a launch.
 #include <cuda_runtime.h>
 

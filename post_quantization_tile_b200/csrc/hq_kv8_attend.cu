@@ -18,9 +18,9 @@
 // value row as the fragments it needs, the boxes' swizzle keeps those reads free of bank conflicts, and
 // nothing is transposed but byte pairs of two value rows and the 8 x 8 tiles of probabilities
 // (movmatrix).  Bound by the codes' bytes on long caches (5.7 TB/s); below some 10 MB by the latency of
-// this kernel and the join (and the weights): 3 x 8 heads x 1500 slots, ten rows, weights: 17.7 us.
+// this kernel and the join (and the weights): 3 x 8 heads x 1500 slots, ten rows, weights: 17.9 us.
 //   - queries become binary16 after a power-of-two scaling per row (bf16's 8 bits fit exactly, elements
-//     below 2^-38 of the row's largest lose bits);
+//     below 2^-31 of the row's largest lose bits);
 //   - probabilities become binary16 at 2^7 times their value relative to a running reference, which
 //     moves up to the maximum when that is more than 2^8 larger: 11 bits, at most 2^15, and weights
 //     down to 2^-31 of the largest still count.  The lanes look for a maximum only when one of them
@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kThreadsA, FewCfg<ROWS>::BLOCKS)
 // The weight each cached slot received, summed over a key head's rows: with the rows' sums known,
 // exp(s - lse) is recomputed from the keys.  One warp takes sixteen slots and walks the rows sixteen at a
 // time, so every slot is summed by four lanes in a fixed order.  Reads the keys once more, half the bytes of
-// the attention itself.
+// the attention itself, and converts the queries again for every sixteen slots: one row over 8 x 32 heads x
+// 8192 slots 327 us with weights, 92 without; 2 x 512 queries x 32 heads over 8192 slots 1.63 ms and 0.18.
 template <int D>
 __global__ void __launch_bounds__(kThreadsA, 2) kv8_weights_kernel(const AttendArgs a)
 {

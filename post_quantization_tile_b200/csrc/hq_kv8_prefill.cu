@@ -10,9 +10,10 @@
 //
 // Warps: 0-3 and 4-7 softmax of the two row tiles, 8-11 conversion, 12 MMA issue.
 //
-// 2 x 512 queries x 32 heads over 8192 slots: 182 us, 0.76 PFLOP/s, tensor pipe 37% and exponentials 38%
-// busy.  Bound by the chain of a step (scores out of TMEM, maximum, exponentials, P back, P V): with half of
-// the score MMAs, without the conversion or without the exponentials it stays at 167 to 175 us.
+// 2 x 512 queries x 32 heads over 8192 slots: 183 us, 0.75 PFLOP/s, tensor pipe 39% and issue slots 41%
+// busy.  In this arrangement, one warpgroup for both score buffers of a row tile, the chain of a step takes the
+// time (scores out of TMEM, maximum, exponentials, P back, P V): with half of the score MMAs, without the conversion
+// or without the exponentials it stayed within 6%.
 //
 // Numerics as in the kernel for few rows (hq_kv8_attend.cu).  One accumulator serves pages of unlike scales, so
 // value codes enter binary16 times 2^-15 .. 2^7, their page's scale (up to the next power of two) over the
