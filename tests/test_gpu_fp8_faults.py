@@ -57,3 +57,18 @@ def test_no_box_is_under_way_after_a_timeout(hq, silent, M, N, K_, block, stages
 def test_no_tensor_core_work_is_under_way_after_a_timeout(hq, silent, M, N, K_, block, stages):
     log = run(hq, silent, M, N, K_, block)
     assert len(log) and torch.all(log[:, 2] == 1)
+
+
+@pytest.mark.parametrize("M,N,K_,block,stages", CASES)
+def test_the_test_librarys_own_product_withholds_nothing(hq, M, N, K_, block, stages):
+    from post_quantization_tile_b200 import build
+    P, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    f = ctypes.CDLL(build.TEST_LIB).hq_gemm_fp8
+    f.argtypes, f.restype = [P, i64, P, i64, P, i64, P, i64, i64, P, i32, P, ctypes.c_size_t, P], i32
+    g = torch.Generator().manual_seed(M)
+    a = hq.fp8_quantize(torch.randn(M, K_, generator=g).cuda())
+    w = hq.fp8_quantize(torch.randn(N, K_, generator=g).cuda(), block=128)
+    y, ws, ld = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), hq.fp8_workspace(), a.data.shape[1]
+    assert f(a.data.data_ptr(), ld, a.scale.data_ptr(), M, w.data.data_ptr(), ld, w.scale.data_ptr(), N, K_, y.data_ptr(), 0, ws.ptr(), ws.nbytes,
+             torch.cuda.current_stream().cuda_stream) == 0
+    assert hq.status(ws)[0] == 0 and torch.equal(y, hq.gemm_fp8(a, w))
