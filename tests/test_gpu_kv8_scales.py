@@ -127,3 +127,53 @@ def test_scores_whose_factor_vanishes_in_binary32(hq, rows, k_exp):
         q = (queries(rows, 1, rows, 64).float() * up).to(torch.bfloat16)
         check(hq, cache, table, 333, q, scale=scale, weights=True)
         cache.k.view(torch.uint8)[int(table[0, 4])] = 0
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("rows,G", [(40, 1), (40, 4), (300, 1)])
+def test_many_units_of_unlike_windows(hq, rows, G, causal, page):
+    """More units than thread blocks, of one to three tiles, whose pages span one to four windows: a thread block goes
+    through several, with and without a second row tile.  The formula in 64 bits on the GPU, the bounds of check()."""
+    B, H, D, P = 60, 5, 64, 384 // page
+    g = torch.Generator().manual_seed(rows + page)
+    pages = B * P
+    codes = [(torch.randint(0, 2, (pages, H, page, D), generator=g) * 0x80 + torch.randint(0, 0x7F, (pages, H, page, D), generator=g))
+             .to(torch.uint8) for _ in range(2)]
+    wide = torch.tensor([0.0, 11.0, 25.0, 40.0])[torch.randint(0, 4, (pages, H), generator=g)]  # octaves either way
+    vs = torch.exp2(torch.round((2 * torch.rand(pages, H, generator=g) - 1) * wide))
+    vs = torch.where(torch.rand(pages, H, generator=g) < 0.1, vs * 0.75, vs).clamp(2.0 ** -40, 2.0 ** 40)
+    cache = hq.Kv8Cache(codes[0].cuda().view(hq.FP8), codes[1].cuda().view(hq.FP8), torch.full((pages, H), 2.0 ** -8).cuda(), vs.cuda())
+    table = torch.randperm(pages, generator=g).to(torch.int32).view(B, P).cuda()
+    lens = torch.randint(0, 385, (B,), generator=g, dtype=torch.int32).cuda()
+    m = torch.randint(0, rows + 1, (B,), generator=g, dtype=torch.int32).cuda()
+    q = torch.randn(B, H * G, rows, D, generator=g).to(torch.bfloat16).cuda()
+    out, lse = torch.full_like(q, 7.0), torch.full((B, H * G, rows), 7.0, device="cuda")
+    hq.kv8_attend(q, cache, table, lens, q_lens=m, causal=causal, out=out, lse=lse)
+    ids = table.long()
+    k, v = ((c.double() * s.double()[:, :, None, None])[ids].transpose(1, 2).reshape(B, H, 384, D)
+            for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    i, j = torch.arange(rows, device="cuda"), torch.arange(384, device="cuda")
+    n, mm = lens[:, None, None].long(), m[:, None, None].long()
+    sees = (j < n) & (j <= i[None, :, None] + (n - mm)) if causal else (j < n).expand(B, rows, 384)
+    for h in range(H * G):
+        x, kk, vv = q[:, h].double(), k[:, h // G], v[:, h // G]
+        s = torch.where(sees, x @ kk.transpose(1, 2) * D ** -0.5, -torch.inf)
+        top = s.amax(2, keepdim=True)
+        some = torch.isfinite(top)
+        p = torch.exp(s - torch.where(some, top, 0.0))
+        total = p.sum(2, keepdim=True)
+        step = torch.where(p > 0, p.clamp(max=2.0 ** -32), 0.0) / total.clamp(min=1e-300)
+        p = p / total.clamp(min=1e-300)
+        size = torch.where(sees, x.abs() @ kk.abs().transpose(1, 2), 0.0).amax(2, keepdim=True)
+        ref_lse = torch.where(some, top + torch.log(total.clamp(min=1e-300)), -torch.inf)[:, :, 0]
+        big = torch.where(sees, s.abs(), 0.0).amax(2, keepdim=True) + torch.where(some, ref_lse[:, :, None].abs(), 0.0)
+        rel = 2 * (D + 4) * 2.0 ** -23 * size * D ** -0.5 + 2.0 ** -20 + 384 * 2.0 ** -24 + 2.0 ** -22 * big
+        ref = p @ vv
+        tol = 2.0 ** -8 * ref.abs() + ((2.0 ** -11 + 2 * rel) * p + step) @ vv.abs()
+        asked = (i < mm[:, 0])
+        err = (out[:, h].double() - ref).abs()
+        assert torch.all((err <= tol) | ~asked[:, :, None]), float(((err / tol.clamp(min=1e-300)) * asked[:, :, None]).max())
+        assert torch.all((out[:, h] == 7.0) | asked[:, :, None]) and torch.all((lse[:, h] == 7.0) | asked)
+        got = lse[:, h].double()
+        assert torch.all((got == ref_lse) | ((got - ref_lse).abs() <= rel[:, :, 0]) | ~asked)
