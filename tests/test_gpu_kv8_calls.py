@@ -168,3 +168,36 @@ def test_causal_without_a_truth_value_raises_its_own_error(hq):
     with pytest.raises(TypeError):
         hq.kv8_attend(q, cache, t, n, scale="wide")
     assert hq.kv8_attend(q, cache, t, n, causal=0).shape == q.shape
+
+
+@pytest.mark.parametrize("rows", [1, 33])
+def test_the_largest_batch(hq, rows):
+    """2048 sequences, most of them short, with few rows and with many."""
+    import numpy as np
+    from test_gpu_kv8 import check_attend
+    rng = np.random.default_rng(rows)
+    lens, asked = rng.integers(0, 20, 2048).tolist(), np.minimum(rng.integers(0, 3, 2048), rows)
+    asked[[0, 1000, 2047]] = rows
+    check_attend(hq, 2048, 1, 1, rows, 64, 16, lens, q_lens=asked.tolist(), seed=rows, P=2)
+
+
+def test_a_pool_of_more_than_32_bits_of_bytes(hq):
+    """Keys of 5.4 GB, values too: sequences on the pool's first and last pages give what they give in a small pool."""
+    H, page, D, far = 4, 64, 128, 164000
+    big, small = hq.alloc_kv8(far + 8, H, D, page), hq.alloc_kv8(16, H, D, page)
+    assert big.k.numel() > 5 << 30
+    high, low = i32([[far + 3, 1, far + 7], [far, far + 5, 0]]), i32([[3, 9, 7], [0, 5, 8]])
+    high_to, low_to = i32([[far + 1], [far + 6]]), i32([[1], [6]])
+    x = torch.randn(2, 2 * H, 150, D, generator=gen(12)).to(torch.bfloat16).cuda()
+    q = torch.randn(2, 2 * H, 40, D, generator=gen(13)).to(torch.bfloat16).cuda()
+    got = []
+    for cache, table, to in ((big, high, high_to), (small, low, low_to)):
+        lens, w = i32([0, 0]), torch.zeros(2, H, 192, device="cuda")
+        hq.kv8_append(cache, x[:, :H, :149], x[:, H:, :149], table, lens)
+        lens += 149
+        hq.kv8_append(cache, x[:, :H, 149:], x[:, H:, 149:], table, lens)
+        lens += 1
+        outs = [hq.kv8_attend(q, cache, table, lens, weights=w, weights_in=w), hq.kv8_attend(q[:, :, :2], cache, table, lens)]
+        n, ow = hq.kv8_evict(cache, table, lens, w, 50, 10, to)
+        got.append(outs + [w, n, ow, hq.kv8_attend(q, cache, to, n)])
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][0].abs().amax() > 0.1
